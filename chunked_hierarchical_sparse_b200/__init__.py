@@ -14,12 +14,15 @@ lse [B, L, h_q, K].
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
 import torch
 
 __all__ = ["hsa_set_wait_limit_ns", "hsa_timing_enable", "hsa_timing_read", "KERNELS", "hsa_workspace_size", "hsa_pool", "hsa_select", "hsa_fwd", "hsa_attend", "hsa_decode", "hsa_decode_multi", "hsa_bwd",
+           "hsa_prompt_workspace_size", "hsa_prompt_fwd", "hsa_prompt_bwd", "hsa_prefix_workspace_size",
+           "hsa_prefix_decode", "HsaPromptShape", "HsaPrefixShape",
            "hsa_device_status", "HsaError", "lib_path", "load_library", "OP_POOL", "OP_SELECT",
            "OP_FWD", "OP_DECODE", "OP_BWD"]
 
@@ -31,7 +34,7 @@ _F32, _BF16 = 0, 1
 # kernel kinds of hsa_timing_read (hsa_kernel_t)
 KERNELS = {"pool": 1, "select": 2, "attend_simt": 3, "decode": 4, "bwd1": 5, "invert": 6, "bwd2": 7,
            "attend_tc": 8, "plan": 9,
-           "bwd_tc": 10, "bwd_sel": 11}
+           "bwd_tc": 10, "bwd_sel": 11, "prompt_fwd": 12, "prompt_bwd": 13, "prefix": 14}
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "workspace too small",
            4: "CUDA launch or API error", 5: "device wait timed out",
            6: "device-side input check failed"}
@@ -45,6 +48,15 @@ class HsaError(RuntimeError):
 
 class HsaShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "L", "h_q", "h_kv", "d", "S", "K", "dtype")]
+
+
+class HsaPromptShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "L", "h_q", "h_kv", "d", "n_seq", "off_by_one", "dtype")]
+
+
+class HsaPrefixShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "P", "cap", "h_q", "h_kv", "d", "off_by_one", "dtype")] + [
+        ("prefix_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -69,6 +81,14 @@ def load_library():
         L.hsa_decode.argtypes = [sp, P, P, P, P, P, P, P, P, P, Z, P]
         L.hsa_decode_multi.argtypes = [sp, ctypes.c_int32, P, P, P, P, P, P, P, P, P, Z, P]
         L.hsa_bwd.argtypes = [sp, P, P, P, P, P, P, P, P, P, P, P, P, P, P, Z, P]
+        pp, xp = ctypes.POINTER(HsaPromptShape), ctypes.POINTER(HsaPrefixShape)
+        L.hsa_prompt_workspace_size.argtypes = [pp, I]
+        L.hsa_prompt_workspace_size.restype = Z
+        L.hsa_prompt_fwd.argtypes = [pp, P, P, P, P, P, P, P, Z, P]
+        L.hsa_prompt_bwd.argtypes = [pp, P, P, P, P, P, P, P, P, P, P, P, Z, P]
+        L.hsa_prefix_workspace_size.argtypes = [xp]
+        L.hsa_prefix_workspace_size.restype = Z
+        L.hsa_prefix_decode.argtypes = [xp, P, P, P, P, P, P, P, P, P, Z, P]
         L.hsa_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_int32), P]
         L.hsa_timing_enable.argtypes = [I]
         L.hsa_timing_read.argtypes = [I, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]
@@ -78,7 +98,8 @@ def load_library():
         L.hsa_status_string.restype = ctypes.c_char_p
         L.hsa_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
         L.hsa_set_wait_limit_ns.restype = ctypes.c_int
-        for f in ("hsa_pool", "hsa_select", "hsa_fwd", "hsa_attend", "hsa_decode", "hsa_decode_multi", "hsa_bwd", "hsa_device_status"):
+        for f in ("hsa_pool", "hsa_select", "hsa_fwd", "hsa_attend", "hsa_decode", "hsa_decode_multi", "hsa_bwd", "hsa_device_status",
+                  "hsa_prompt_fwd", "hsa_prompt_bwd", "hsa_prefix_decode"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -144,6 +165,10 @@ def _workspace(sh: HsaShape, op: int, device, ws):
     n = int(load_library().hsa_workspace_size(ctypes.byref(sh), op))
     if n == 0:
         raise HsaError(1, "hsa_workspace_size")
+    return _workspace_bytes(n, device, ws)
+
+
+def _workspace_bytes(n: int, device, ws):
     if ws is not None:
         if not isinstance(ws, torch.Tensor) or ws.device != device or not ws.is_contiguous():
             raise ValueError(f"workspace: a contiguous tensor on {device} is required")
@@ -301,6 +326,152 @@ def hsa_bwd(q, k, v, q_slc, dO, lse, idx, w, kbar, K: int, S: int = 64, ws=None,
     _run("hsa_bwd", dev, stream, ctypes.byref(sh), _p(q), _p(k), _p(v), _p(q_slc), _p(dO), _p(lse),
          _p(idx), _p(w), _p(kbar), _p(dq), _p(dk), _p(dv), _p(dqs), _p(w_), n)
     return dq, dk, dv, dqs
+
+
+# ------------------------------------------------------------------ dense attention
+def _allocating(dev, stream):
+    """Allocate outputs and workspace on the stream that the call runs on: their memory
+    is then not in use by another stream's earlier work, nor reused before the call ends."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _out(t, name, shape, dtype, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, shape, dtype, dev)
+    return t
+
+
+def _prompt_shape(q, k, v, cu_seqlens, off_by_one):
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, L, h_q, d] tensor")
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a [B, h_kv, L, d] tensor")
+    B, L, h_q, d = q.shape
+    h_kv, dt, dev = k.shape[1], _dtype_code(q), q.device
+    _need(q, "q", q.shape, q.dtype)
+    _need(k, "k", (B, h_kv, L, d), q.dtype, dev)
+    _need(v, "v", (B, h_kv, L, d), q.dtype, dev)
+    n_seq = 0
+    if cu_seqlens is not None:
+        n_seq = cu_seqlens.numel() - 1
+        if n_seq < 1 or B != 1:
+            raise ValueError("cu_seqlens: at least two entries, with every sequence packed into one batch row (B = 1)")
+        _need(cu_seqlens, "cu_seqlens", (n_seq + 1,), torch.int32, dev)
+    return HsaPromptShape(B, L, h_q, h_kv, d, n_seq, 1 if off_by_one else 0, dt)
+
+
+def hsa_prompt_workspace_size(B, L, h_q, h_kv, d, dtype, op, n_seq: int = 0) -> int:
+    sh = HsaPromptShape(B, L, h_q, h_kv, d, n_seq, 0, _BF16 if dtype == torch.bfloat16 else _F32)
+    n = int(load_library().hsa_prompt_workspace_size(ctypes.byref(sh), op))
+    if n == 0:
+        raise HsaError(2, "hsa_prompt_workspace_size")
+    return n
+
+
+def _prompt_ws(sh, op, dev, ws):
+    n = int(load_library().hsa_prompt_workspace_size(ctypes.byref(sh), op))
+    if n == 0:
+        raise HsaError(2, "hsa_prompt_workspace_size")
+    return _workspace_bytes(n, dev, ws)
+
+
+def hsa_prompt_fwd(q, k, v, cu_seqlens=None, off_by_one: bool = False, want_lse: bool = True, o=None, lse=None,
+                   ws=None, stream=None):
+    """Causal attention over whole prompts.  q [B,L,h_q,d], k, v [B,h_kv,L,d]; each batch
+    row is one prompt, or (B = 1) cu_seqlens (int32, on the GPU) gives the bounds of the
+    prompts packed into it.  Returns (o, lse); rows outside every prompt keep what o and
+    lse held (a tensor that the call allocates is not initialised there)."""
+    sh = _prompt_shape(q, k, v, cu_seqlens, off_by_one)
+    B, L, h_q, _ = q.shape
+    dev = q.device
+    with _allocating(dev, stream):
+        o = _out(o, "o", q.shape, q.dtype, dev)
+        if lse is not None or want_lse:
+            lse = _out(lse, "lse", (B, L, h_q), torch.float32, dev)
+        w_, n = _prompt_ws(sh, OP_FWD, dev, ws)
+        _run("hsa_prompt_fwd", dev, stream, ctypes.byref(sh), _p(q), _p(k), _p(v), _p(cu_seqlens), _p(o), _p(lse),
+             _p(w_), n)
+    return o, lse
+
+
+def hsa_prompt_bwd(q, k, v, o, dO, lse, cu_seqlens=None, dq=None, dk=None, dv=None, ws=None, stream=None):
+    """Backward of hsa_prompt_fwd (o and lse as it returned them, with or without
+    off_by_one).  Returns (dq, dk, dv); rows outside every prompt as in the forward."""
+    sh = _prompt_shape(q, k, v, cu_seqlens, False)
+    dev = q.device
+    _need(o, "o", q.shape, q.dtype, dev)
+    _need(dO, "dO", q.shape, q.dtype, dev)
+    _need(lse, "lse", q.shape[:3], torch.float32, dev)
+    with _allocating(dev, stream):
+        dq = _out(dq, "dq", q.shape, q.dtype, dev)
+        dk = _out(dk, "dk", k.shape, q.dtype, dev)
+        dv = _out(dv, "dv", v.shape, q.dtype, dev)
+        w_, n = _prompt_ws(sh, OP_BWD, dev, ws)
+        _run("hsa_prompt_bwd", dev, stream, ctypes.byref(sh), _p(q), _p(k), _p(v), _p(o), _p(dO), _p(lse),
+             _p(cu_seqlens), _p(dq), _p(dk), _p(dv), _p(w_), n)
+    return dq, dk, dv
+
+
+def hsa_prefix_workspace_size(B, P, cap, h_q, h_kv, d, dtype) -> int:
+    sh = HsaPrefixShape(B, P, cap, h_q, h_kv, d, 0, _BF16 if dtype == torch.bfloat16 else _F32, P * d)
+    n = int(load_library().hsa_prefix_workspace_size(ctypes.byref(sh)))
+    if n == 0:
+        raise HsaError(2, "hsa_prefix_workspace_size")
+    return n
+
+
+def _prefix_planes(t, name, h_kv, d, dtype, dev):
+    """A [h_kv, P, d] prefix whose planes may lie further apart than P*d (the first P
+    tokens of a longer buffer); returns the elements between planes."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[0] != h_kv or t.shape[2] != d:
+        raise ValueError(f"{name} must be a [{h_kv}, P, {d}] tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    P = t.shape[1]
+    if P and (t.stride(2) != 1 or (P > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the tokens of a group must be contiguous")
+    return t.stride(0) if h_kv > 1 and P else P * d
+
+
+def hsa_prefix_decode(q, k_prefix, v_prefix, k_cache, v_cache, lens, off_by_one: bool = False, want_lse: bool = True,
+                      o=None, lse=None, ws=None, stream=None):
+    """One decode step of sequences that share their first P tokens.  q [B,h_q,d];
+    k_prefix, v_prefix [h_kv,P,d] (for example the first P tokens of one prompt's k[0],
+    v[0] in hsa_prompt_fwd); k_cache, v_cache [B,h_kv,cap,d] with the lens[b] (int32, on
+    the GPU) tokens that sequence b has of its own.  Returns (o, lse)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [B, h_q, d] tensor")
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a [B, h_kv, cap, d] tensor")
+    B, h_q, d = q.shape
+    h_kv, cap = k_cache.shape[1], k_cache.shape[2]
+    dt, dev = _dtype_code(q), q.device
+    _need(q, "q", q.shape, q.dtype)
+    _need(k_cache, "k_cache", (B, h_kv, cap, d), q.dtype, dev)
+    _need(v_cache, "v_cache", (B, h_kv, cap, d), q.dtype, dev)
+    _need(lens, "lens", (B,), torch.int32, dev)
+    stride = _prefix_planes(k_prefix, "k_prefix", h_kv, d, q.dtype, dev)
+    if v_prefix.shape != k_prefix.shape or _prefix_planes(v_prefix, "v_prefix", h_kv, d, q.dtype, dev) != stride:
+        raise ValueError("v_prefix must have k_prefix's shape and strides")
+    sh = HsaPrefixShape(B, k_prefix.shape[1], cap, h_q, h_kv, d, 1 if off_by_one else 0, dt, stride)
+    n = int(load_library().hsa_prefix_workspace_size(ctypes.byref(sh)))
+    if n == 0:
+        raise HsaError(2, "hsa_prefix_workspace_size")
+    with _allocating(dev, stream):
+        o = _out(o, "o", q.shape, q.dtype, dev)
+        if lse is not None or want_lse:
+            lse = _out(lse, "lse", (B, h_q), torch.float32, dev)
+        w_, n = _workspace_bytes(n, dev, ws)
+        _run("hsa_prefix_decode", dev, stream, ctypes.byref(sh), _p(q), _p(k_prefix), _p(v_prefix), _p(k_cache),
+             _p(v_cache), _p(lens), _p(o), _p(lse), _p(w_), n)
+    return o, lse
 
 
 def hsa_device_status(ws: torch.Tensor, stream=None) -> int:

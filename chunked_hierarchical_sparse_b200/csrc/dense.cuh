@@ -1,0 +1,178 @@
+// dense.cuh -- dense attention: the causal prompt pass and its backward, and the
+// decode step over a shared prefix.  Work items, their enumeration and the
+// launchers shared by the CUDA-core and the tensor-core kernels.
+//
+// Rows.  The G query heads of a group read the same keys, so a tile's rows are
+// (token, head) pairs: row r is token r / G and head g*G + r % G.  q's layout
+// [.., token, head, d] makes such a tile one box of consecutive memory per token.
+#pragma once
+
+#include "hsa_internal.cuh"
+
+namespace hsa {
+namespace dense {
+
+constexpr int kSimtRows = 64;    // rows and keys of a CUDA-core tile
+constexpr int kNoMask = 0x3fffffff;  // causal offset of an item whose keys are all visible
+
+// Geometry and tensors of one call (passed to the kernels by value).
+struct Args {
+    int decode;                  // 0: prompt pass, 1: decode over a shared prefix
+    int B, L, hq, hkv, G;        // decode: L = P (prefix tokens)
+    int tok;                     // tokens per row tile
+    int off_by_one;
+    float scale, scale_log2;     // 1 / sqrt(d), and that times log2(e)
+    // prompt pass
+    const int4 *plan;            // packed: {first token, tokens, tile, 0} per tile, dearest first (else null)
+    const int32_t *plan_n;       //         entries in `plan`
+    int tiles;                   // not packed: row tiles per batch row
+    // decode
+    int cap;                     // tokens of a sequence's own cache
+    const int32_t *lens;         // [B]
+    int pre_tiles, pre_sub, pre_slots;  // prefix: row tiles, keys per slot, slots
+    int suf_sub, suf_slots;             // own caches: keys per slot, slots
+    // tensors: 0 = the prompt's (or the prefix's) keys and values, 1 = the own caches'
+    const void *q, *k[2], *v[2];
+    int64_t plane[2];            // elements between two (batch, group) planes of k[i] / v[i]
+    void *o;
+    float *lse;
+    float *po, *plse;            // decode partials [slots][B*hq][d] and [slots][B*hq]
+    DevStatus *ds;
+};
+
+// One row tile and the range of keys it reads.
+struct Item {
+    int tok0, ntok;   // first token row (of [B*L] or, decode, of [B]) and tokens
+    int g;            // KV group
+    int src;          // which k / v
+    int plane;        // (batch, group) plane of k / v
+    int key0, nkeys;  // first key and number of keys
+    int off;          // row of token i sees key j (both relative) iff j <= off + i
+    int slot;         // decode: partial slot
+};
+
+__device__ __forceinline__ int own_len(const Args &a, int b) {
+    const int n = a.lens[b];
+    if (n >= 0 && n <= a.cap) return n;
+    report(a.ds, HSA_ERR_DEVICE_CHECK, kKDense, b, n);
+    return min(max(n, 0), a.cap);
+}
+
+__device__ __forceinline__ int item_count(const Args &a) {
+    if (a.decode) return a.hkv * (a.pre_tiles * a.pre_slots + a.B * a.suf_slots);
+    return a.plan ? *a.plan_n * a.hkv : a.B * a.hkv * a.tiles;
+}
+
+// Item i of the call, dearest first; false when it has no rows or no keys.
+__device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
+    if (!a.decode) {
+        int start, len, tile, b;
+        if (a.plan) {
+            const int4 p = a.plan[i / a.hkv];
+            it.g = i % a.hkv;
+            b = 0; start = p.x; len = p.y; tile = p.z;
+        } else {
+            const int bh = i % (a.B * a.hkv);
+            b = bh / a.hkv;
+            it.g = bh % a.hkv;
+            start = 0; len = a.L; tile = a.tiles - 1 - i / (a.B * a.hkv);
+        }
+        const int t = tile * a.tok;
+        it.tok0 = b * a.L + start + t;
+        it.ntok = min(a.tok, len - t);
+        it.src = 0;
+        it.plane = b * a.hkv + it.g;
+        it.key0 = start;
+        it.nkeys = t + it.ntok;
+        it.off = t;
+        it.slot = 0;
+        return it.ntok > 0;
+    }
+    it.off = kNoMask;
+    const int npre = a.hkv * a.pre_tiles * a.pre_slots;
+    if (i < npre) {
+        it.g = i % a.hkv;
+        const int r = i / a.hkv, tile = r % a.pre_tiles, s = r / a.pre_tiles;
+        it.tok0 = tile * a.tok;
+        it.ntok = min(a.tok, a.B - it.tok0);
+        it.src = 0;
+        it.plane = it.g;
+        it.key0 = s * a.pre_sub;
+        it.nkeys = min(a.pre_sub, a.L - it.key0);
+        it.slot = s;
+    } else {
+        i -= npre;
+        it.g = i % a.hkv;
+        const int r = i / a.hkv;
+        it.tok0 = r % a.B;
+        it.ntok = 1;
+        const int s = r / a.B;
+        it.src = 1;
+        it.plane = it.tok0 * a.hkv + it.g;
+        it.key0 = s * a.suf_sub;
+        it.nkeys = min(a.suf_sub, own_len(a, it.tok0) - it.key0);
+        it.slot = a.pre_slots + s;
+    }
+    return it.ntok > 0 && it.nkeys > 0;
+}
+
+// ------------------------------------------------------------------ launchers
+// Packed prompts: the tiles of `tok` tokens of every sequence, dearest first
+// (first_dear: the cost of a sequence's tiles falls with their index -- the tiles
+// of keys of the backward -- instead of rising).  A cu_seqlens that does not rise
+// inside [0, L] is reported and gives no tiles.
+cudaError_t launch_plan(const int32_t *cu, int n_seq, int L, int tok, bool first_dear, int4 *plan, int32_t *plan_n,
+                        DevStatus *ds, cudaStream_t st);
+inline int64_t plan_cap(int L, int n_seq, int tok) { return (int64_t)L / tok + n_seq; }
+
+struct BwdArgs {
+    Args a;                      // a.plan: the row tiles; a.q, a.k, a.v as in the forward
+    const int4 *kplan;           // packed: the key tiles
+    const int32_t *kplan_n;
+    int ktiles;                  // not packed: key tiles per batch row
+    const void *o, *dO;
+    const float *lse;
+    float *delta;                // [B*L, h_q]  dO . o
+    void *dq, *dk, *dv;
+};
+
+// One tile of keys of the backward and the sequence whose rows read it.
+struct KeyItem {
+    int64_t row0;       // token row (of [B*L]) of the sequence's first token
+    int start, len;     // the sequence inside its batch row
+    int n0, nkeys;      // first key (of the sequence) and keys
+    int g, plane;
+};
+
+__device__ __forceinline__ int key_item_count(const BwdArgs &b) {
+    return b.kplan ? *b.kplan_n * b.a.hkv : b.a.B * b.a.hkv * b.ktiles;
+}
+
+// Key item i (dearest first: the first keys are read by the most rows) of tiles of `keys`.
+__device__ __forceinline__ bool get_key_item(const BwdArgs &b, int i, int keys, KeyItem &it) {
+    int tile, row;
+    if (b.kplan) {
+        const int4 p = b.kplan[i / b.a.hkv];
+        it.g = i % b.a.hkv;
+        row = 0; it.start = p.x; it.len = p.y; tile = p.z;
+    } else {
+        const int bh = i % (b.a.B * b.a.hkv);
+        row = bh / b.a.hkv;
+        it.g = bh % b.a.hkv;
+        it.start = 0; it.len = b.a.L; tile = i / (b.a.B * b.a.hkv);
+    }
+    it.row0 = (int64_t)row * b.a.L + it.start;
+    it.n0 = tile * keys;
+    it.nkeys = min(keys, it.len - it.n0);
+    it.plane = row * b.a.hkv + it.g;
+    return it.nkeys > 0;
+}
+
+cudaError_t launch_fwd_simt(const Args &a, int d, bool bf16, int64_t max_items, cudaStream_t st);
+cudaError_t launch_combine(const Args &a, int d, bool bf16, cudaStream_t st);
+cudaError_t launch_delta(const BwdArgs &b, int d, bool bf16, cudaStream_t st);
+cudaError_t launch_bwd_simt(const BwdArgs &b, int d, bool bf16, int64_t max_row_items, int64_t max_key_items,
+                            cudaStream_t st);
+
+}  // namespace dense
+}  // namespace hsa

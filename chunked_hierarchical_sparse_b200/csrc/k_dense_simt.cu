@@ -1,0 +1,390 @@
+// k_dense_simt.cu -- dense attention and its backward on the CUDA cores.
+//
+// A block takes one tile of 64 (token, head) rows of a group and walks the keys
+// in tiles of 64 (the key-major backward kernel: a tile of 64 keys, walking the
+// rows).  Every product of a tile pair is a 64 x 64 (or 64 x d) fp32 outer-product
+// loop out of shared memory: thread (ty, tx) of 16 x 16 owns rows ty + 16 i and
+// columns tx + 16 j, so that the lanes of a warp read different rows of a padded
+// tile (stride d + 4 floats: 16-byte reads without bank conflicts).  Softmax state
+// (running maximum, sum, output) stays in fp32 registers.
+//
+// Bound: FFMA issue fed by shared memory (8 16-byte reads per 64 FMAs); the tiles
+// of keys come from L2 and cost little beside it.
+#include "dense.cuh"
+
+namespace hsa {
+namespace dense {
+
+namespace {
+
+constexpr int kT = kSimtRows;
+constexpr int kThr = 256;
+constexpr int kPS = kT + 4;  // row stride of a 64 x 64 tile
+
+template <typename T> __device__ __forceinline__ float4 load4(const T *p);
+template <> __device__ __forceinline__ float4 load4<float>(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
+}
+template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+
+// 64 rows of d values into a padded tile; row r comes from src(r) (null: zeros)
+template <int D, typename T, typename F> __device__ __forceinline__ void load_tile(float *dst, F &&src) {
+    constexpr int V = D / 4;
+    for (int i = threadIdx.x; i < kT * V; i += kThr) {
+        const int r = i / V, c = (i % V) * 4;
+        const T *p = src(r);
+        const float4 x = p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = x;
+    }
+}
+
+// acc[i][j] = A[ty + 16 i] . B[tx + 16 j] over d
+template <int D> __device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float *A, const float *B, int ty, int tx) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * (D + 4) + c);
+            y[i] = *reinterpret_cast<const float4 *>(B + (tx + 16 * i) * (D + 4) + c);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
+                acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
+                acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
+                acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+            }
+    }
+}
+
+// acc[i][64 h + 4 tx + e] += sum_n P(n, i) B[n][..]; P(n, i) is P[ty + 16 i][n], or P[n][ty + 16 i]
+template <int D, bool TRANSPOSED>
+__device__ __forceinline__ void accum_tile(float (&acc)[4][D / 16], const float *P, const float *B, int ty, int tx) {
+#pragma unroll 2
+    for (int n = 0; n < kT; n += 4) {
+        float p[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (TRANSPOSED) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[i][e] = P[(n + e) * kPS + ty + 16 * i];
+            } else {
+                const float4 v = *reinterpret_cast<const float4 *>(P + (ty + 16 * i) * kPS + n);
+                p[i][0] = v.x; p[i][1] = v.y; p[i][2] = v.z; p[i][3] = v.w;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+                const float4 b = *reinterpret_cast<const float4 *>(B + (n + e) * (D + 4) + h * 64 + tx * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[i][h * 4 + 0] = fmaf(p[i][e], b.x, acc[i][h * 4 + 0]);
+                    acc[i][h * 4 + 1] = fmaf(p[i][e], b.y, acc[i][h * 4 + 1]);
+                    acc[i][h * 4 + 2] = fmaf(p[i][e], b.z, acc[i][h * 4 + 2]);
+                    acc[i][h * 4 + 3] = fmaf(p[i][e], b.w, acc[i][h * 4 + 3]);
+                }
+            }
+    }
+}
+
+__device__ __forceinline__ float row_max16(float x) {  // over the 16 lanes that share a row
+#pragma unroll
+    for (int o = 8; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+__device__ __forceinline__ float row_sum16(float x) {
+#pragma unroll
+    for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+template <typename T> __device__ __forceinline__ void store4(T *p, float4 v) {
+    Elem<T>::store(p, v.x); Elem<T>::store(p + 1, v.y); Elem<T>::store(p + 2, v.z); Elem<T>::store(p + 3, v.w);
+}
+template <> __device__ __forceinline__ void store4<float>(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ Args a) {
+    extern __shared__ float sm[];
+    float *Q = sm, *K = Q + kT * (D + 4), *V = K + kT * (D + 4), *P = V + kT * (D + 4);
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    Item it;
+    if ((int64_t)blockIdx.x >= item_count(a) || !get_item(a, blockIdx.x, it)) return;
+    const int rows = it.ntok * a.G;
+    const T *q = static_cast<const T *>(a.q);
+    const T *kp = static_cast<const T *>(a.k[it.src]) + it.plane * a.plane[it.src] + (int64_t)it.key0 * D;
+    const T *vp = static_cast<const T *>(a.v[it.src]) + it.plane * a.plane[it.src] + (int64_t)it.key0 * D;
+    auto row_index = [&](int r) { return ((int64_t)it.tok0 + r / a.G) * a.hq + it.g * a.G + r % a.G; };
+    load_tile<D, T>(Q, [&](int r) -> const T * { return r < rows ? q + row_index(r) * D : nullptr; });
+    float m[4], z[4], o[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        z[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+    }
+    for (int n0 = 0; n0 < it.nkeys; n0 += kT) {
+        __syncthreads();
+        auto key = [&](const T *p, int r) -> const T * { return n0 + r < it.nkeys ? p + (int64_t)(n0 + r) * D : nullptr; };
+        load_tile<D, T>(K, [&](int r) { return key(kp, r); });
+        load_tile<D, T>(V, [&](int r) { return key(vp, r); });
+        __syncthreads();
+        float s[4][4];
+        dot_tile<D>(s, Q, K, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int last = it.off + (ty + 16 * i) / a.G;  // this row's last visible key
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = n0 + tx + 16 * j;
+                s[i][j] = n < it.nkeys && n <= last ? s[i][j] * a.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+            mx = fmaxf(m[i], row_max16(mx));
+            const float ms = mx == -INFINITY ? 0.f : mx;
+            const float f = exp2f(m[i] - ms);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[i][j] - ms);
+                sum += p;
+                P[(ty + 16 * i) * kPS + tx + 16 * j] = p;
+            }
+            z[i] = z[i] * f + row_sum16(sum);
+            m[i] = mx;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
+        }
+        __syncthreads();
+        accum_tile<D, false>(o, P, V, ty, tx);
+    }
+    const int64_t nrow = (int64_t)a.B * a.hq;  // decode rows per slot
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty + 16 * i;
+        if (r >= rows) continue;
+        const int64_t ri = row_index(r);
+        float mm = m[i] == -INFINITY ? 0.f : m[i], zz = z[i], f = 1.f;
+        if (!a.decode && a.off_by_one) {  // the added 1 is a logit of 0
+            const float top = fmaxf(mm, 0.f);
+            f = exp2f(mm - top);
+            zz = zz * f + exp2f(-top);
+            mm = top;
+        }
+        const float inv = zz > 0.f ? f / zz : (zz == 0.f ? 0.f : zz);
+        const float l = (mm + log2f(zz)) * 0.6931471805599453f;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+            const float4 v = make_float4(o[i][h * 4] * inv, o[i][h * 4 + 1] * inv, o[i][h * 4 + 2] * inv, o[i][h * 4 + 3] * inv);
+            const int c = h * 64 + tx * 4;
+            if (a.decode) store4<float>(a.po + (it.slot * nrow + ri) * D + c, v);
+            else store4<T>(static_cast<T *>(a.o) + ri * D + c, v);
+        }
+        if (tx == 0) {
+            if (a.decode) a.plse[it.slot * nrow + ri] = l;
+            else if (a.lse) a.lse[ri] = l;
+        }
+    }
+}
+
+// delta[row] = dO . o, one warp per (token, head) row
+template <typename T, int D>
+__global__ void __launch_bounds__(256) delta_kernel(const T *o, const T *dO, float *delta, int64_t rows) {
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (r >= rows) return;
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < D; c += 128) {
+        if (c + lane * 4 < D) {
+            const float4 x = load4<T>(o + r * D + c + lane * 4), y = load4<T>(dO + r * D + c + lane * 4);
+            s += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+        }
+    }
+    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if (lane == 0) delta[r] = s;
+}
+
+// dq of a row tile: walks the keys, dq += (p (dO.v - delta)) k
+template <typename T, int D>
+__global__ void __launch_bounds__(kThr) bwd_dq_simt_kernel(const __grid_constant__ BwdArgs b) {
+    extern __shared__ float sm[];
+    const Args &a = b.a;
+    float *Q = sm, *G = Q + kT * (D + 4), *K = G + kT * (D + 4), *V = K + kT * (D + 4), *S = V + kT * (D + 4);
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    Item it;
+    if ((int64_t)blockIdx.x >= item_count(a) || !get_item(a, blockIdx.x, it)) return;
+    const int rows = it.ntok * a.G;
+    const int64_t pl = it.plane * a.plane[0] + (int64_t)it.key0 * D;
+    const T *kp = static_cast<const T *>(a.k[0]) + pl, *vp = static_cast<const T *>(a.v[0]) + pl;
+    auto row_index = [&](int r) { return ((int64_t)it.tok0 + r / a.G) * a.hq + it.g * a.G + r % a.G; };
+    load_tile<D, T>(Q, [&](int r) -> const T * { return r < rows ? static_cast<const T *>(a.q) + row_index(r) * D : nullptr; });
+    load_tile<D, T>(G, [&](int r) -> const T * { return r < rows ? static_cast<const T *>(b.dO) + row_index(r) * D : nullptr; });
+    float l2[4], de[4], dq[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty + 16 * i;
+        l2[i] = r < rows ? b.lse[row_index(r)] * 1.4426950408889634f : INFINITY;
+        de[i] = r < rows ? b.delta[row_index(r)] : 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) dq[i][c] = 0.f;
+    }
+    for (int n0 = 0; n0 < it.nkeys; n0 += kT) {
+        __syncthreads();
+        auto key = [&](const T *p, int r) -> const T * { return n0 + r < it.nkeys ? p + (int64_t)(n0 + r) * D : nullptr; };
+        load_tile<D, T>(K, [&](int r) { return key(kp, r); });
+        load_tile<D, T>(V, [&](int r) { return key(vp, r); });
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        dot_tile<D>(s, Q, K, ty, tx);
+        dot_tile<D>(dp, G, V, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int last = it.off + (ty + 16 * i) / a.G;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = n0 + tx + 16 * j;
+                const float p = exp2f(s[i][j] * a.scale_log2 - l2[i]);
+                S[(ty + 16 * i) * kPS + tx + 16 * j] = n < it.nkeys && n <= last ? p * (dp[i][j] - de[i]) : 0.f;
+            }
+        }
+        __syncthreads();
+        accum_tile<D, false>(dq, S, K, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty + 16 * i;
+        if (r >= rows) continue;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+            store4<T>(static_cast<T *>(b.dq) + row_index(r) * D + h * 64 + tx * 4,
+                      make_float4(dq[i][h * 4] * a.scale, dq[i][h * 4 + 1] * a.scale, dq[i][h * 4 + 2] * a.scale,
+                                  dq[i][h * 4 + 3] * a.scale));
+    }
+}
+
+// dk, dv of a tile of keys: walks the row tiles that see it, all heads of the group
+template <typename T, int D>
+__global__ void __launch_bounds__(kThr) bwd_dkv_simt_kernel(const __grid_constant__ BwdArgs b) {
+    extern __shared__ float sm[];
+    const Args &a = b.a;
+    float *K = sm, *V = K + kT * (D + 4), *Q = V + kT * (D + 4), *G = Q + kT * (D + 4), *P = G + kT * (D + 4),
+          *S = P + kT * kPS;
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    KeyItem it;
+    if ((int64_t)blockIdx.x >= key_item_count(b) || !get_key_item(b, blockIdx.x, kT, it)) return;
+    const int64_t pl = it.plane * a.plane[0] + (int64_t)(it.start + it.n0) * D;
+    load_tile<D, T>(K, [&](int r) -> const T * { return r < it.nkeys ? static_cast<const T *>(a.k[0]) + pl + r * D : nullptr; });
+    load_tile<D, T>(V, [&](int r) -> const T * { return r < it.nkeys ? static_cast<const T *>(a.v[0]) + pl + r * D : nullptr; });
+    float dk[4][D / 16], dv[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
+    for (int t0 = it.n0; t0 < it.len; t0 += a.tok) {
+        const int rows = min(a.tok, it.len - t0) * a.G;
+        auto row_index = [&](int r) { return (it.row0 + t0 + r / a.G) * a.hq + it.g * a.G + r % a.G; };
+        __syncthreads();
+        load_tile<D, T>(Q, [&](int r) -> const T * { return r < rows ? static_cast<const T *>(a.q) + row_index(r) * D : nullptr; });
+        load_tile<D, T>(G, [&](int r) -> const T * { return r < rows ? static_cast<const T *>(b.dO) + row_index(r) * D : nullptr; });
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        dot_tile<D>(s, Q, K, ty, tx);
+        dot_tile<D>(dp, G, V, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty + 16 * i;
+            const float l2 = r < rows ? b.lse[row_index(r)] * 1.4426950408889634f : INFINITY;
+            const float de = r < rows ? b.delta[row_index(r)] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = tx + 16 * j;
+                const bool seen = r < rows && n < it.nkeys && it.n0 + n <= t0 + r / a.G;
+                const float p = seen ? exp2f(s[i][j] * a.scale_log2 - l2) : 0.f;
+                P[r * kPS + n] = p;
+                S[r * kPS + n] = seen ? p * (dp[i][j] - de) : 0.f;
+            }
+        }
+        __syncthreads();
+        accum_tile<D, true>(dv, P, G, ty, tx);
+        accum_tile<D, true>(dk, S, Q, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = ty + 16 * i;
+        if (n >= it.nkeys) continue;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+            const int64_t at = pl + (int64_t)n * D + h * 64 + tx * 4;
+            store4<T>(static_cast<T *>(b.dv) + at, make_float4(dv[i][h * 4], dv[i][h * 4 + 1], dv[i][h * 4 + 2], dv[i][h * 4 + 3]));
+            store4<T>(static_cast<T *>(b.dk) + at,
+                      make_float4(dk[i][h * 4] * a.scale, dk[i][h * 4 + 1] * a.scale, dk[i][h * 4 + 2] * a.scale,
+                                  dk[i][h * 4 + 3] * a.scale));
+        }
+    }
+}
+
+template <int D> constexpr size_t fwd_smem() { return sizeof(float) * (3 * kT * (D + 4) + kT * kPS); }
+template <int D> constexpr size_t dq_smem() { return sizeof(float) * (4 * kT * (D + 4) + kT * kPS); }
+template <int D> constexpr size_t dkv_smem() { return sizeof(float) * (4 * kT * (D + 4) + 2 * kT * kPS); }
+
+template <typename T, int D> cudaError_t fwd(const Args &a, int64_t items, cudaStream_t st) {
+    cudaError_t e = set_smem_once((const void *)fwd_simt_kernel<T, D>, fwd_smem<D>());
+    if (e != cudaSuccess) return e;
+    fwd_simt_kernel<T, D><<<(unsigned)items, kThr, fwd_smem<D>(), st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int D> cudaError_t delta(const BwdArgs &b, cudaStream_t st) {
+    const int64_t rows = (int64_t)b.a.B * b.a.L * b.a.hq;
+    delta_kernel<T, D><<<(unsigned)ceil_div(rows, 8), 256, 0, st>>>(static_cast<const T *>(b.o),
+                                                                    static_cast<const T *>(b.dO), b.delta, rows);
+    return cudaGetLastError();
+}
+
+template <typename T, int D> cudaError_t bwd(const BwdArgs &b, int64_t row_items, int64_t key_items, cudaStream_t st) {
+    cudaError_t e = set_smem_once((const void *)bwd_dq_simt_kernel<T, D>, dq_smem<D>());
+    if (e == cudaSuccess) e = set_smem_once((const void *)bwd_dkv_simt_kernel<T, D>, dkv_smem<D>());
+    if (e != cudaSuccess) return e;
+    bwd_dkv_simt_kernel<T, D><<<(unsigned)key_items, kThr, dkv_smem<D>(), st>>>(b);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    bwd_dq_simt_kernel<T, D><<<(unsigned)row_items, kThr, dq_smem<D>(), st>>>(b);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_fwd_simt(const Args &a, int d, bool bf16, int64_t items, cudaStream_t st) {
+    if (bf16) return d == 128 ? fwd<__nv_bfloat16, 128>(a, items, st) : fwd<__nv_bfloat16, 64>(a, items, st);
+    return d == 128 ? fwd<float, 128>(a, items, st) : fwd<float, 64>(a, items, st);
+}
+
+cudaError_t launch_delta(const BwdArgs &b, int d, bool bf16, cudaStream_t st) {
+    if (bf16) return d == 128 ? delta<__nv_bfloat16, 128>(b, st) : delta<__nv_bfloat16, 64>(b, st);
+    return d == 128 ? delta<float, 128>(b, st) : delta<float, 64>(b, st);
+}
+
+cudaError_t launch_bwd_simt(const BwdArgs &b, int d, bool bf16, int64_t row_items, int64_t key_items, cudaStream_t st) {
+    if (bf16)
+        return d == 128 ? bwd<__nv_bfloat16, 128>(b, row_items, key_items, st)
+                        : bwd<__nv_bfloat16, 64>(b, row_items, key_items, st);
+    return d == 128 ? bwd<float, 128>(b, row_items, key_items, st) : bwd<float, 64>(b, row_items, key_items, st);
+}
+
+}  // namespace dense
+}  // namespace hsa

@@ -191,6 +191,93 @@ HSA_API hsa_status_t hsa_bwd(const hsa_shape_t *shape, const void *q, const void
                      const float *w, const float *kbar, void *dq, void *dk, void *dv,
                      void *dq_slc, void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Dense attention beside the sparse one.  HSA leaves a token's own chunk and
+ * everything its top-K leaves out to the layers around it, and [P3] measures it
+ * against full attention; these calls are those layers' attention, in the same
+ * layouts: causal attention over whole prompts with its backward, and the decode
+ * step of a batch whose sequences share a long prefix.
+ *
+ * x_tj = q[t,h] . k[g,j] / sqrt(d) for head h of group g = floor(h / (h_q/h_kv)).
+ * With off_by_one = 0, Z_t = sum_j e^{x_tj} (softmax); with off_by_one = 1,
+ * Z_t = 1 + sum_j e^{x_tj} (softmax-off-by-one, as inside a chunk of hsa_fwd).
+ * o_t = sum_j e^{x_tj} v_j / Z_t and lse_t = log Z_t.  A row without any key has
+ * o = 0 and lse = log Z (-infinity, or 0 with off_by_one).
+ * d in {64, 128}, h_q % h_kv == 0, h_q / h_kv <= 16, fp32 or bf16.  Logits,
+ * softmax statistics and all sums are fp32; in bf16 the probabilities (and, in
+ * the backward, their gradients) are rounded to bf16 as operands of the second
+ * product, the usual choice for tensor cores.  Results are the same bit for bit
+ * on every call. */
+
+typedef struct {
+    int32_t B;          /* batch rows                                            */
+    int32_t L;          /* tokens per batch row                                  */
+    int32_t h_q;        /* query heads                                           */
+    int32_t h_kv;       /* KV heads = query groups                               */
+    int32_t d;          /* head dimension                                        */
+    int32_t n_seq;      /* 0: each batch row is one sequence of L tokens; else   */
+                        /* the number of sequences packed into the one row (B=1) */
+    int32_t off_by_one; /* 0 or 1                                                */
+    int32_t dtype;      /* hsa_dtype_t                                           */
+} hsa_prompt_shape_t;
+
+/* Workspace bytes of hsa_prompt_fwd (op = HSA_OP_FWD) or hsa_prompt_bwd
+ * (HSA_OP_BWD); 0 for an invalid shape.  256-byte aligned, status word first,
+ * as for hsa_workspace_size. */
+HSA_API size_t hsa_prompt_workspace_size(const hsa_prompt_shape_t *shape, int op);
+
+/* Causal attention over whole prompts: token t attends to the tokens j <= t of
+ * its own sequence.  q, o [B,L,h_q,d]; k, v [B,h_kv,L,d]; lse [B,L,h_q] fp32
+ * (optional, needed by the backward).  cu_seqlens (device, [n_seq+1] int32; NULL
+ * with n_seq = 0): sequence s is the tokens cu_seqlens[s] .. cu_seqlens[s+1]-1;
+ * it must rise (equal neighbours: an empty sequence) within [0, L], otherwise
+ * HSA_ERR_DEVICE_CHECK is reported and nothing is written.  Rows outside every
+ * sequence are neither read nor written.  A NaN or infinity in q, k or v at
+ * token t reaches the rows of its own sequence only; in v at token t also rows
+ * up to 127 tokens before it may become NaN (masked weights are zeros of a
+ * matrix product). */
+HSA_API hsa_status_t hsa_prompt_fwd(const hsa_prompt_shape_t *shape, const void *q, const void *k,
+                                    const void *v, const int32_t *cu_seqlens, void *o, float *lse,
+                                    void *ws, size_t ws_bytes, void *stream);
+
+/* Backward of hsa_prompt_fwd: gradients of sum(dO * o), from its inputs and its
+ * o and lse (which carry off_by_one).  dq [B,L,h_q,d], dk, dv [B,h_kv,L,d], all
+ * required; rows outside every sequence are neither read nor written. */
+HSA_API hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, const void *k,
+                                    const void *v, const void *o, const void *dO, const float *lse,
+                                    const int32_t *cu_seqlens, void *dq, void *dk, void *dv, void *ws,
+                                    size_t ws_bytes, void *stream);
+
+typedef struct {
+    int32_t B;          /* sequences                                             */
+    int32_t P;          /* tokens of the shared prefix (may be 0)                */
+    int32_t cap;        /* tokens each sequence's own cache can hold (may be 0)  */
+    int32_t h_q;
+    int32_t h_kv;
+    int32_t d;
+    int32_t off_by_one; /* 0 or 1                                                */
+    int32_t dtype;      /* hsa_dtype_t                                           */
+    int64_t prefix_stride; /* elements from one group's prefix to the next's     */
+} hsa_prefix_shape_t;
+
+HSA_API size_t hsa_prefix_workspace_size(const hsa_prefix_shape_t *shape);
+
+/* One decode step of a batch whose sequences all begin with the same P tokens:
+ * each sequence's new token attends to the prefix and to the lens[b] tokens of
+ * its own behind it (its own key and value among them, if they are to count).
+ * The prefix is read once for all sequences.  q, o [B,h_q,d]; k_prefix, v_prefix
+ * [h_kv,P,d] with group planes prefix_stride >= P*d elements apart (a multiple
+ * of 16 bytes), so that they may be the first P tokens of longer buffers such as
+ * hsa_prompt_fwd's k and v; k_cache, v_cache [B,h_kv,cap,d], of which the tokens
+ * from lens[b] on are never used (they may hold anything); lens (device, [B]
+ * int32) in [0, cap], otherwise HSA_ERR_DEVICE_CHECK is reported and the nearest
+ * bound taken; lse [B,h_q] fp32, optional.  The prefix pointers may be NULL with
+ * P = 0, the cache pointers and lens with cap = 0. */
+HSA_API hsa_status_t hsa_prefix_decode(const hsa_prefix_shape_t *shape, const void *q,
+                                       const void *k_prefix, const void *v_prefix, const void *k_cache,
+                                       const void *v_cache, const int32_t *lens, void *o, float *lse,
+                                       void *ws, size_t ws_bytes, void *stream);
+
 /* hsa_fwd without a caller-provided workspace.  The source pages have no
  * counterpart to this call; it exists for callers that cannot allocate device
  * memory where they run the forward pass -- e.g. a plug-in inside an inference
@@ -246,6 +333,9 @@ typedef enum {
     HSA_K_PLAN = 9,        /* chunk-major work planning                      */
     HSA_K_BWD_TC = 10,     /* chunk-major backward (tcgen05): dq, dw, dk, dv */
     HSA_K_BWD_SEL = 11,    /* stick-breaking backward + finishing pass       */
+    HSA_K_PROMPT_FWD = 12, /* dense prompt attention (+ work list if packed) */
+    HSA_K_PROMPT_BWD = 13, /* its backward                                   */
+    HSA_K_PREFIX = 14,     /* shared-prefix decode step                      */
     HSA_K_COUNT = 16
 } hsa_kernel_t;
 
