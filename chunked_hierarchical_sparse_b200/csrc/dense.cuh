@@ -29,8 +29,11 @@ struct Args {
     // decode
     int cap;                     // tokens of a sequence's own cache
     const int32_t *lens;         // [B]
-    int pre_tiles, pre_sub, pre_slots;  // prefix: row tiles, keys per slot, slots
-    int suf_sub, suf_slots;             // own caches: keys per slot, slots
+    // The prefix is cut into pre_slots slots of pre_sub keys, each own cache into suf_slots
+    // of suf_sub; a slot's attention is one partial.  An item takes `per` slots at a time
+    // (one per stream of the tensor-core kernel, where the streams split the keys).
+    int pre_tiles, pre_sub, pre_slots, pre_per;
+    int suf_sub, suf_slots, suf_per;
     // tensors: 0 = the prompt's (or the prefix's) keys and values, 1 = the own caches'
     const void *q, *k[2], *v[2];
     int64_t plane[2];            // elements between two (batch, group) planes of k[i] / v[i]
@@ -48,7 +51,8 @@ struct Item {
     int plane;        // (batch, group) plane of k / v
     int key0, nkeys;  // first key and number of keys
     int off;          // row of token i sees key j (both relative) iff j <= off + i
-    int slot;         // decode: partial slot
+    int slot;         // decode: (first) partial slot
+    int foreign;      // the last tile of 128 keys reaches beyond this sequence's own
 };
 
 __device__ __forceinline__ int own_len(const Args &a, int b) {
@@ -58,8 +62,15 @@ __device__ __forceinline__ int own_len(const Args &a, int b) {
     return min(max(n, 0), a.cap);
 }
 
+__host__ __device__ __forceinline__ int pre_items(const Args &a) {
+    return a.pre_slots ? (a.pre_slots + a.pre_per - 1) / a.pre_per : 0;
+}
+__host__ __device__ __forceinline__ int suf_items(const Args &a) {
+    return a.suf_slots ? (a.suf_slots + a.suf_per - 1) / a.suf_per : 0;
+}
+
 __device__ __forceinline__ int item_count(const Args &a) {
-    if (a.decode) return a.hkv * (a.pre_tiles * a.pre_slots + a.B * a.suf_slots);
+    if (a.decode) return a.hkv * (a.pre_tiles * pre_items(a) + a.B * suf_items(a));
     return a.plan ? *a.plan_n * a.hkv : a.B * a.hkv * a.tiles;
 }
 
@@ -86,10 +97,12 @@ __device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
         it.nkeys = t + it.ntok;
         it.off = t;
         it.slot = 0;
+        it.foreign = (it.nkeys + 127) / 128 * 128 > len;
         return it.ntok > 0;
     }
     it.off = kNoMask;
-    const int npre = a.hkv * a.pre_tiles * a.pre_slots;
+    it.foreign = 1;
+    const int npre = a.hkv * a.pre_tiles * pre_items(a);
     if (i < npre) {
         it.g = i % a.hkv;
         const int r = i / a.hkv, tile = r % a.pre_tiles, s = r / a.pre_tiles;
@@ -97,9 +110,9 @@ __device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
         it.ntok = min(a.tok, a.B - it.tok0);
         it.src = 0;
         it.plane = it.g;
-        it.key0 = s * a.pre_sub;
-        it.nkeys = min(a.pre_sub, a.L - it.key0);
-        it.slot = s;
+        it.slot = s * a.pre_per;
+        it.key0 = it.slot * a.pre_sub;
+        it.nkeys = min(a.pre_per * a.pre_sub, a.L - it.key0);
     } else {
         i -= npre;
         it.g = i % a.hkv;
@@ -109,9 +122,9 @@ __device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
         const int s = r / a.B;
         it.src = 1;
         it.plane = it.tok0 * a.hkv + it.g;
-        it.key0 = s * a.suf_sub;
-        it.nkeys = min(a.suf_sub, own_len(a, it.tok0) - it.key0);
-        it.slot = a.pre_slots + s;
+        it.slot = a.pre_slots + s * a.suf_per;
+        it.key0 = s * a.suf_per * a.suf_sub;
+        it.nkeys = min(a.suf_per * a.suf_sub, own_len(a, it.tok0) - it.key0);
     }
     return it.ntok > 0 && it.nkeys > 0;
 }
@@ -169,6 +182,9 @@ __device__ __forceinline__ bool get_key_item(const BwdArgs &b, int i, int keys, 
 }
 
 cudaError_t launch_fwd_simt(const Args &a, int d, bool bf16, int64_t max_items, cudaStream_t st);
+// bf16, on the tensor cores: a.tok is two row tiles (128 / G tokens each), but for a
+// decode call whose batch fits one; `next` is a zero int32, the items dealt so far.
+cudaError_t launch_fwd_tc(const Args &a, int d, int64_t items, int32_t *next, cudaStream_t st);
 cudaError_t launch_combine(const Args &a, int d, bool bf16, cudaStream_t st);
 cudaError_t launch_delta(const BwdArgs &b, int d, bool bf16, cudaStream_t st);
 cudaError_t launch_bwd_simt(const BwdArgs &b, int d, bool bf16, int64_t max_row_items, int64_t max_key_items,

@@ -34,7 +34,7 @@ struct Carver {
 };
 
 // words of the workspace header behind the status word (all cleared by every call)
-constexpr int kWordPlanN = 8, kWordKPlanN = 9;
+constexpr int kWordPlanN = 8, kWordKPlanN = 9, kWordNext = 32;
 int32_t *word(void *ws, int i) { return static_cast<int32_t *>(ws) + i; }
 
 hsa_status_t check_heads(int h_q, int h_kv, int d, int off_by_one, int dtype) {
@@ -63,12 +63,18 @@ struct PromptWs {
     size_t bytes;
 };
 
-int row_tile(const hsa_prompt_shape_t &s) { return kSimtRows / (s.h_q / s.h_kv); }
+// tokens of a row item: 64 rows on the CUDA cores (fp32), two tiles of 128 rows on the
+// tensor cores (bf16)
+int row_tile(const hsa_prompt_shape_t &s) {
+    const int G = s.h_q / s.h_kv;
+    return s.dtype == HSA_BF16 ? 2 * (128 / G) : kSimtRows / G;
+}
+int bwd_row_tile(const hsa_prompt_shape_t &s) { return kSimtRows / (s.h_q / s.h_kv); }
 
 PromptWs carve_prompt(const hsa_prompt_shape_t &s, void *ws, bool bwd) {
     Carver c{static_cast<char *>(ws)};
     PromptWs w{};
-    if (s.n_seq > 0) w.plan = c.take<int4>(plan_cap(s.L, s.n_seq, row_tile(s)));
+    if (s.n_seq > 0) w.plan = c.take<int4>(plan_cap(s.L, s.n_seq, bwd ? bwd_row_tile(s) : row_tile(s)));
     if (bwd) {
         if (s.n_seq > 0) w.kplan = c.take<int4>(plan_cap(s.L, s.n_seq, kSimtRows));
         w.delta = c.take<float>((size_t)s.B * s.L * s.h_q);
@@ -77,10 +83,11 @@ PromptWs carve_prompt(const hsa_prompt_shape_t &s, void *ws, bool bwd) {
     return w;
 }
 
-Args prompt_args(const hsa_prompt_shape_t &s, const void *q, const void *k, const void *v, void *ws, const PromptWs &w) {
+Args prompt_args(const hsa_prompt_shape_t &s, const void *q, const void *k, const void *v, void *ws, const PromptWs &w,
+                 int tok) {
     Args a{};
     a.B = s.B; a.L = s.L; a.hq = s.h_q; a.hkv = s.h_kv; a.G = s.h_q / s.h_kv;
-    a.tok = row_tile(s);
+    a.tok = tok;
     a.off_by_one = s.off_by_one;
     a.scale = 1.0f / sqrtf((float)s.d);
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.d));
@@ -114,7 +121,7 @@ hsa_status_t check_prompt_call(const hsa_prompt_shape_t *shape, const int32_t *c
 constexpr int kSms = 148;
 
 struct PrefixPlan {
-    int tok, pre_tiles, pre_sub, pre_slots, suf_sub, suf_slots;
+    int tok, pre_tiles, pre_sub, pre_slots, pre_per, suf_sub, suf_slots, suf_per;
     size_t po, plse, bytes;  // workspace offsets
 };
 
@@ -130,20 +137,27 @@ hsa_status_t check_prefix(const hsa_prefix_shape_t *s) {
     return HSA_OK;
 }
 
-// keys per slot: about two waves of blocks over `jobs` independent jobs, in whole tiles
-int split(int64_t keys, int64_t jobs, int tile) {
+// keys per slot: about `want` slots in all for `jobs` independent jobs of `keys` keys, in whole tiles
+int split(int64_t keys, int64_t jobs, int64_t want, int tile) {
     if (keys == 0) return 0;
-    const int64_t n = std::clamp<int64_t>(2 * kSms / std::max<int64_t>(jobs, 1), 1, ceil_div(keys, tile));
+    const int64_t n = std::clamp<int64_t>(want / std::max<int64_t>(jobs, 1), 1, ceil_div(keys, tile));
     return (int)round_up(ceil_div(keys, n), tile);
 }
 
 PrefixPlan plan_prefix(const hsa_prefix_shape_t &s) {
     PrefixPlan p{};
-    p.tok = kSimtRows / (s.h_q / s.h_kv);
+    const bool tc = s.dtype == HSA_BF16;
+    const int G = s.h_q / s.h_kv, keys = tc ? 128 : kSimtRows, fit = (tc ? 128 : kSimtRows) / G;
+    // tensor cores: a batch beyond one row tile shares the keys between two row tiles,
+    // a smaller one (and every own cache) splits them between the two streams
+    const bool pair = tc && s.B > fit;
+    p.tok = pair ? 2 * fit : fit;
+    p.pre_per = tc && !pair ? 2 : 1;
+    p.suf_per = tc ? 2 : 1;
     p.pre_tiles = (int)ceil_div(s.B, p.tok);
-    p.pre_sub = split(s.P, (int64_t)s.h_kv * p.pre_tiles, kSimtRows);
+    p.pre_sub = split(s.P, (int64_t)s.h_kv * p.pre_tiles, 2 * kSms, keys);
     p.pre_slots = p.pre_sub ? (int)ceil_div(s.P, p.pre_sub) : 0;
-    p.suf_sub = split(s.cap, (int64_t)s.h_kv * s.B, kSimtRows);
+    p.suf_sub = split(s.cap, (int64_t)s.h_kv * s.B, 2 * kSms, keys);
     p.suf_slots = p.suf_sub ? (int)ceil_div(s.cap, p.suf_sub) : 0;
     Carver c{nullptr};
     const size_t rows = (size_t)s.B * s.h_q * (p.pre_slots + p.suf_slots);
@@ -174,13 +188,16 @@ hsa_status_t hsa_prompt_fwd(const hsa_prompt_shape_t *shape, const void *q, cons
     cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeader, st);
     if (empty || e != cudaSuccess) return cuda_status(e);
     const PromptWs w = carve_prompt(*shape, ws, false);
-    Args a = prompt_args(*shape, q, k, v, ws, w);
+    Args a = prompt_args(*shape, q, k, v, ws, w, row_tile(*shape));
     a.o = o;
     a.lse = lse;
     TimedLaunch tl(HSA_K_PROMPT_FWD, cu_seqlens ? 2 : 1, st);
     if (cu_seqlens) e = launch_plan(cu_seqlens, shape->n_seq, shape->L, a.tok, false, w.plan, word(ws, kWordPlanN), a.ds, st);
-    if (e == cudaSuccess)
-        e = launch_fwd_simt(a, shape->d, shape->dtype == HSA_BF16, max_items(*shape, a.tok), st);
+    if (e == cudaSuccess) {
+        const int64_t items = max_items(*shape, a.tok);
+        e = shape->dtype == HSA_BF16 ? launch_fwd_tc(a, shape->d, items, word(ws, kWordNext), st)
+                                     : launch_fwd_simt(a, shape->d, false, items, st);
+    }
     return cuda_status(e);
 }
 
@@ -197,7 +214,7 @@ hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, cons
     const PromptWs w = carve_prompt(*shape, ws, true);
     const bool bf16 = shape->dtype == HSA_BF16;
     BwdArgs b{};
-    b.a = prompt_args(*shape, q, k, v, ws, w);
+    b.a = prompt_args(*shape, q, k, v, ws, w, bwd_row_tile(*shape));
     b.kplan = w.kplan;
     b.kplan_n = word(ws, kWordKPlanN);
     b.ktiles = (int)ceil_div(shape->L, kSimtRows);
@@ -245,8 +262,8 @@ hsa_status_t hsa_prefix_decode(const hsa_prefix_shape_t *shape, const void *q, c
     a.scale = 1.0f / sqrtf((float)shape->d);
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)shape->d));
     a.cap = shape->cap; a.lens = lens;
-    a.pre_tiles = p.pre_tiles; a.pre_sub = p.pre_sub; a.pre_slots = p.pre_slots;
-    a.suf_sub = p.suf_sub; a.suf_slots = p.suf_slots;
+    a.pre_tiles = p.pre_tiles; a.pre_sub = p.pre_sub; a.pre_slots = p.pre_slots; a.pre_per = p.pre_per;
+    a.suf_sub = p.suf_sub; a.suf_slots = p.suf_slots; a.suf_per = p.suf_per;
     a.q = q;
     a.k[0] = k_prefix; a.v[0] = v_prefix; a.plane[0] = shape->prefix_stride;
     a.k[1] = k_cache; a.v[1] = v_cache; a.plane[1] = (int64_t)shape->cap * shape->d;
@@ -254,9 +271,11 @@ hsa_status_t hsa_prefix_decode(const hsa_prefix_shape_t *shape, const void *q, c
     a.po = reinterpret_cast<float *>(static_cast<char *>(ws) + p.po);
     a.plse = reinterpret_cast<float *>(static_cast<char *>(ws) + p.plse);
     a.ds = static_cast<DevStatus *>(ws);
-    const int64_t items = (int64_t)a.hkv * ((int64_t)a.pre_tiles * a.pre_slots + (int64_t)a.B * a.suf_slots);
+    const int64_t items = (int64_t)a.hkv * ((int64_t)a.pre_tiles * pre_items(a) + (int64_t)a.B * suf_items(a));
     TimedLaunch tl(HSA_K_PREFIX, items > 0 ? 2 : 1, st);
-    if (items > 0) e = launch_fwd_simt(a, shape->d, bf16, items, st);
+    if (items > 0)
+        e = bf16 ? launch_fwd_tc(a, shape->d, items, word(ws, kWordNext), st)
+                 : launch_fwd_simt(a, shape->d, false, items, st);
     if (e == cudaSuccess) e = launch_combine(a, shape->d, bf16, st);
     return cuda_status(e);
 }

@@ -1,0 +1,520 @@
+// k_dense_fwd_tc.cu -- dense attention on the tensor cores (bf16): the prompt pass
+// and the partial passes of the shared-prefix decode step.
+//
+// Mathematics.  For a tile of 128 (token, head) rows, keys in tiles of 128:
+// S = Q K^T, p = 2^(s c - m), l += sum p, O += P V with c = log2(e)/sqrt(d), one
+// pass over the keys; o = O / l, lse = (m + log2 l) ln 2.  m is a running
+// maximum that is only moved (and O, l rescaled) when a tile exceeds it by more
+// than 2^8: p then stays below 256, which neither fp32 sums nor bf16 operands
+// mind, and O in tensor memory is almost never touched.
+//
+// One persistent CTA per SM with two streams, each a 128-row tile with its own S
+// and O in tensor memory and its own softmax warpgroup (one thread per row, the
+// whole row of S in registers; P goes back over S's columns as bf16 and feeds the
+// second product from there).  While one stream's softmax works, the tensor cores
+// run the other's products; the MMAs of a stream are issued in the order
+// P.V(j), S(j+1), so S may overwrite the P that the product before it reads, and
+// a finished S(j+1) means that O holds tiles 0..j.
+// - Prompt pass: the streams are neighbouring row tiles and share the K and V tiles.
+// - Decode, more rows than one tile (prefix): likewise.
+// - Decode otherwise: both streams hold the same rows and take half of the keys each.
+// Warp 8 deals the items (dynamically, dearest first) and loads by TMA, warp 9
+// issues the MMAs.
+#include "dense_tc.cuh"
+
+namespace hsa {
+namespace dense {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kKeys = 128;        // keys per tile
+constexpr int kWarpLoad = 8, kWarpMma = 9;
+constexpr int kItems = 2;         // item ring
+constexpr float kSlack = 8.f;     // log2 of how far a tile may exceed m before it moves
+
+template <int D> struct Smem {
+    static constexpr int NH = D / 64;                 // 64-column halves
+    static constexpr int TILE = NH * 128 * 128;       // bytes of a 128 x D bf16 tile
+    static constexpr int ST = D == 128 ? 5 : 10;      // K / V tile ring
+    static constexpr int OFF_Q = 0;                   // [2]
+    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_ITEM = OFF_KV + ST * TILE;
+    static constexpr int OFF_BAR = OFF_ITEM + kItems * 128;
+    static constexpr int OFF_MISC = OFF_BAR + 512;
+    static constexpr int ALLOC = OFF_MISC + 64 + 1024;  // + alignment to 1 KB
+};
+static_assert(Smem<128>::ALLOC <= 232448 && Smem<64>::ALLOC <= 232448, "shared memory of a CTA");
+
+struct TcItem {
+    int end, src, plane, g, one, shared, foreign;  // one: load the single token's rows only
+    int tok[2], ntok[2], key0[2], nkeys[2], off[2], slot[2];
+};
+static_assert(sizeof(TcItem) <= 128, "item ring");
+
+// Item i of the call as two streams; false when neither has rows and keys.
+__device__ __forceinline__ bool get_tc_item(const Args &a, int i, TcItem &t) {
+    Item it;
+    const bool some = get_item(a, i, it);
+    const int tt = a.decode ? (it.slot >= a.pre_slots ? 1 : 128 / a.G) : a.tok / 2;  // tokens of one stream's tile
+    t.end = 0; t.src = it.src; t.plane = it.plane; t.g = it.g; t.one = 0;
+    t.shared = !a.decode || (it.src == 0 && a.pre_per == 1);
+    t.foreign = it.foreign;
+    if (t.shared) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            t.tok[s] = it.tok0 + s * tt;
+            t.ntok[s] = min(tt, it.ntok - s * tt);
+            t.key0[s] = it.key0;
+            t.off[s] = it.off == kNoMask ? kNoMask : it.off + s * tt;
+            t.nkeys[s] = t.ntok[s] <= 0 ? 0 : (it.off == kNoMask ? it.nkeys : min(it.nkeys, t.off[s] + t.ntok[s]));
+            t.slot[s] = it.slot;
+        }
+    } else {  // the item's keys are two slots, one per stream
+        const int sub = it.src ? a.suf_sub : a.pre_sub;
+        t.one = it.src;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            t.tok[s] = it.tok0;
+            t.ntok[s] = it.ntok;
+            t.key0[s] = it.key0 + s * sub;
+            t.off[s] = kNoMask;
+            t.nkeys[s] = max(0, min(sub, it.nkeys - s * sub));
+            t.slot[s] = it.slot + s;
+        }
+    }
+    return some;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
+    const __grid_constant__ CUtensorMap tm_k0, const __grid_constant__ CUtensorMap tm_v0,
+    const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_v1,
+    const __grid_constant__ Args a, int32_t *next, uint64_t wait_ns) {
+    using L = Smem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    TcItem *items = reinterpret_cast<TcItem *>(sm + L::OFF_ITEM);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
+    uint64_t *item_full = bar, *item_empty = bar + kItems;
+    uint64_t *q_full = item_empty + kItems, *q_empty = q_full + 2;
+    uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2;
+    uint64_t *done = o_full + 2;
+    uint64_t *kv_full = done + 1, *kv_empty = kv_full + L::ST;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kItems; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 9); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
+            mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1);
+        }
+        mbar_init(done, 1);
+        for (int i = 0; i < L::ST; ++i) { mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1); }
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == kWarpLoad && lane == 0) {
+        prefetch_tmap(&tm_q); prefetch_tmap(&tm_k0); prefetch_tmap(&tm_v0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto wait = [&](uint64_t *b, uint32_t par, int role) { return warp_wait(b, par & 1, wait_ns, abort_flag, a.ds, role); };
+    auto tiles = [](int keys) { return (keys + kKeys - 1) / kKeys; };
+
+    if (warp >= 8) {
+        reg_dec<56>();
+        if (warp == kWarpLoad) {
+            // ======================================================== items and loads
+            const int total = item_count(a);
+            int idx = blockIdx.x, kv = 0, nq[2] = {0, 0};
+            bool ok = true;
+            auto next_item = [&]() -> int {  // the first gridDim.x items are dealt by block index
+                int i = 0;
+                if (lane == 0) i = atomicAdd(next, 1);
+                return __shfl_sync(0xffffffffu, i, 0) + gridDim.x;
+            };
+            for (int n = 0; ok; ++n) {
+                TcItem t;
+                while (idx < total && !get_tc_item(a, idx, t)) idx = next_item();
+                if (idx >= total) t.end = 1;
+                const int ib = n % kItems;
+                if (n >= kItems && !(ok = wait(&item_empty[ib], n / kItems - 1, 1))) break;
+                if (lane == 0) {
+                    items[ib] = t;
+                    mbar_arrive(&item_full[ib]);  // release: the item is visible to those who wait
+                }
+                __syncwarp();
+                if (t.end) break;
+                const CUtensorMap *mk = t.src ? &tm_k1 : &tm_k0, *mv = t.src ? &tm_v1 : &tm_v0;
+                auto load_q = [&](int s) -> bool {
+                    if (t.nkeys[s] == 0) return true;
+                    if (nq[s] > 0 && !wait(&q_empty[s], nq[s] - 1, 1)) return false;
+                    if (lane == 0) {
+                        const int rows = t.one ? a.G : a.G * (128 / a.G);
+                        mbar_arrive_expect_tx(&q_full[s], L::NH * rows * 128);
+#pragma unroll
+                        for (int h = 0; h < L::NH; ++h)
+                            tma_load_3d(sm + L::OFF_Q + s * L::TILE + h * 16384, t.one ? &tm_q1 : &tm_q, h * 64, t.g * a.G,
+                                        t.tok[s], &q_full[s]);
+                    }
+                    ++nq[s];
+                    return true;
+                };
+                auto load_kv = [&](const CUtensorMap *m, int key) -> bool {
+                    const int st = kv % L::ST;
+                    if (kv >= L::ST && !wait(&kv_empty[st], kv / L::ST - 1, 1)) return false;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&kv_full[st], L::TILE);
+#pragma unroll
+                        for (int h = 0; h < L::NH; ++h)
+                            tma_load_3d(sm + L::OFF_KV + st * L::TILE + h * 16384, m, h * 64, key, t.plane, &kv_full[st]);
+                    }
+                    ++kv;
+                    return true;
+                };
+                const int n0 = tiles(t.nkeys[0]), n1 = tiles(t.nkeys[1]);
+                if (t.shared) {
+                    const int nn = max(n0, n1);
+                    ok = load_q(0) && load_kv(mk, t.key0[0]) && load_q(1);
+                    for (int j = 0; ok && j < nn; ++j) {
+                        ok = load_kv(mv, t.key0[0] + j * kKeys);
+                        if (ok && j + 1 < nn) ok = load_kv(mk, t.key0[0] + (j + 1) * kKeys);
+                    }
+                } else {
+                    ok = load_q(0) && load_kv(mk, t.key0[0]);
+                    if (ok && n1) ok = load_q(1) && load_kv(mk, t.key0[1]);
+                    for (int j = 0; ok && j < n0; ++j) {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const int ns = s ? n1 : n0;
+                            if (ok && j < ns) ok = load_kv(mv, t.key0[s] + j * kKeys);
+                            if (ok && j + 1 < ns) ok = load_kv(mk, t.key0[s] + (j + 1) * kKeys);
+                        }
+                    }
+                }
+                idx = next_item();
+            }
+            if (!ok && lane == 0) {  // the loads in flight land before the CTA goes away (bounded)
+                for (int i = max(0, kv - L::ST); i < kv; ++i) mbar_wait(&kv_full[i % L::ST], (i / L::ST) & 1, kDrainWaitNs);
+                for (int s = 0; s < 2; ++s)
+                    if (nq[s]) mbar_wait(&q_full[s], (nq[s] - 1) & 1, kDrainWaitNs);
+            }
+            __syncwarp();
+        } else if (warp == kWarpMma) {
+            // ======================================================== MMA issue
+            constexpr uint32_t id_s = idesc_bf16_f32(128, kKeys, false, false);
+            constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
+            int kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+            bool ok = true;
+            for (int n = 0; ok; ++n) {
+                const int ib = n % kItems;
+                if (!(ok = wait(&item_full[ib], n / kItems, 2))) break;
+                const TcItem t = items[ib];
+                __syncwarp();
+                mbar_arrive_lane0(&item_empty[ib], lane);
+                if (t.end) break;
+                const int n0 = tiles(t.nkeys[0]), n1 = tiles(t.nkeys[1]), nn = max(n0, n1);
+                // ring positions: shared -- K(j) = base + 2 j, V(j) = base + 2 j + 1; else in order of use
+                const int base = kv;
+                int k_at[2], v_at = 0;  // position of the K tile that S(s) uses next
+                if (t.shared) {
+                    k_at[0] = k_at[1] = base;
+                } else {
+                    k_at[0] = base;
+                    k_at[1] = base + 1;
+                    kv = base + (n1 ? 2 : 1);
+                }
+                auto scores = [&](int s, int j, int ns) -> bool {  // S(s) of tile j
+                    const int st = k_at[s] % L::ST;
+                    if (j == 0 && !wait(&q_full[s], nq[s], 2)) return false;
+                    if (!wait(&kv_full[st], k_at[s] / L::ST, 2)) return false;
+                    if (lane == 0) {
+                        tc_fence_after();
+                        const uint32_t qa = smem_u32(sm + L::OFF_Q + s * L::TILE);
+                        const uint32_t kb = smem_u32(sm + L::OFF_KV + st * L::TILE);
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            mma_bf16_ss(tmem + s * 128, smem_desc_sw128(qa + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                                        smem_desc_sw128(kb + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), id_s, ks > 0);
+                        mma_commit(&s_full[s]);
+                        if (j == ns - 1) mma_commit(&q_empty[s]);
+                        // the K tile is free once the last stream that reads it has
+                        if (!t.shared || s == 1 || j >= n1) mma_commit(&kv_empty[st]);
+                    }
+                    if (j == ns - 1) ++nq[s];
+                    return true;
+                };
+                ok = scores(0, 0, n0);
+                if (ok && n1) ok = scores(1, 0, n1);
+                for (int j = 0; ok && j < nn; ++j) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const int ns = s ? n1 : n0;
+                        if (!ok || j >= ns) continue;
+                        v_at = t.shared ? base + 2 * j + 1 : kv++;
+                        const int st = v_at % L::ST;
+                        if (!(ok = wait(&kv_full[st], v_at / L::ST, 2))) break;
+                        // values behind the last key belong to something else and may be anything:
+                        // their weights are 0, and 0 * NaN is NaN, so they are cleared
+                        if (t.foreign && (t.shared ? j == nn - 1 && s == (n0 != nn) : j == ns - 1)) {
+                            const int last = t.shared ? max(t.nkeys[0], t.nkeys[1]) : t.nkeys[s];
+                            const int r0 = last - j * kKeys;
+                            uint8_t *vb = sm + L::OFF_KV + st * L::TILE;
+                            for (int i = r0 * 8 + lane; i < kKeys * 8; i += 32)
+#pragma unroll
+                                for (int h = 0; h < L::NH; ++h)
+                                    *reinterpret_cast<uint4 *>(vb + h * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        if (!(ok = wait(&p_full[s], np[s], 2))) break;
+                        ++np[s];
+                        if (lane == 0) {
+                            tc_fence_after();
+                            const uint32_t vb = smem_u32(sm + L::OFF_KV + st * L::TILE);
+#pragma unroll
+                            for (int ks = 0; ks < kKeys / 16; ++ks)
+                                mma_bf16_ts(tmem + 256 + s * D, tmem + s * 128 + ks * 8,
+                                            smem_desc_sw128(vb + ks * 2048, 16384, 1024), id_o, j > 0 || ks > 0);
+                            if (!t.shared || s == 1 || j >= n1) mma_commit(&kv_empty[st]);
+                            if (j == ns - 1) mma_commit(&o_full[s]);
+                        }
+                        if (j + 1 < ns) {
+                            k_at[s] = t.shared ? base + 2 * (j + 1) : kv++;
+                            ok = scores(s, j + 1, ns);
+                        }
+                    }
+                }
+                if (t.shared) kv = base + 2 * nn;
+            }
+            if (!ok && lane == 0) {  // the MMAs issued so far end before tensor memory is freed (bounded)
+                mma_commit(done);
+                mbar_wait(done, 0, kDrainWaitNs);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ============================================================ softmax, one warpgroup per stream
+        reg_inc<224>();
+        const int s = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256 + s * D;
+        const int rt = r / a.G, rh = r % a.G;
+        const float c = a.scale_log2;
+        int ns_done = 0, no_done = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const int ib = n % kItems;
+            if (!(ok = wait(&item_full[ib], n / kItems, 3))) break;
+            const int end = items[ib].end, g = items[ib].g, tok = items[ib].tok[s], ntok = items[ib].ntok[s],
+                      nkeys = items[ib].nkeys[s], off = items[ib].off[s], slot = items[ib].slot[s];
+            __syncwarp();
+            mbar_arrive_lane0(&item_empty[ib], lane);
+            if (end) break;
+            const int nt = tiles(nkeys);
+            if (nt == 0) continue;
+            const bool warp_rows = (warp & 3) * 32 < ntok * a.G;  // some row of this warp is real
+            const int lim = min(nkeys - 1, off + rt);             // last key this row sees
+            const int lim_all = min(nkeys - 1, off);              // ... that every row sees
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < nt; ++j) {
+                if (!(ok = wait(&s_full[s], ns_done, 3))) break;
+                ++ns_done;
+                if (warp_rows) {
+                    tc_fence_after();
+                    float x[128];
+                    {
+                        float(&x0)[32] = *reinterpret_cast<float(*)[32]>(x);
+                        float(&x1)[32] = *reinterpret_cast<float(*)[32]>(x + 32);
+                        float(&x2)[32] = *reinterpret_cast<float(*)[32]>(x + 64);
+                        float(&x3)[32] = *reinterpret_cast<float(*)[32]>(x + 96);
+                        tmem_ld32(ts, x0);
+                        tmem_ld32(ts + 32, x1);
+                        tmem_ld32(ts + 64, x2);
+                        tmem_ld32(ts + 96, x3);
+                        tmem_wait_ld();
+                    }
+                    if (j * kKeys + kKeys - 1 > lim_all) {
+                        const int last = lim - j * kKeys;
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) x[i] = i <= last ? x[i] : -INFINITY;
+                    }
+                    float mx0 = x[0], mx1 = x[1];
+#pragma unroll
+                    for (int i = 2; i < 128; i += 4) {
+                        mx0 = fmaxf(mx0, fmaxf(x[i], i + 2 < 128 ? x[i + 2] : x[i]));
+                        mx1 = fmaxf(mx1, fmaxf(x[i + 1], i + 3 < 128 ? x[i + 3] : x[i + 1]));
+                    }
+                    const float mx = fmaxf(mx0, mx1) * c;
+                    if (j == 0) {
+                        m = mx;
+                    } else if (__any_sync(0xffffffffu, mx > m + kSlack)) {
+                        const float f = mx > m + kSlack ? ex2(m - mx) : 1.f;
+                        m = mx > m + kSlack ? mx : m;
+                        l *= f;
+                        // S(j) is complete, so P.V(j-1) issued before it is, too
+#pragma unroll
+                        for (int h = 0; h < D / 32; ++h) {
+                            float y[32];
+                            uint32_t u[32];
+                            tmem_ld32(to + h * 32, y);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(y[i] * f);
+                            tmem_st32(to + h * 32, u);
+                        }
+                    }
+                    const float mn = m == -INFINITY ? 0.f : -m;
+                    const float2 c2 = make_float2(c, c), m2 = make_float2(mn, mn);
+                    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t u[32];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const int e = h * 64 + 2 * i;
+                            float2 y0 = fma2(make_float2(x[e], x[e + 1]), c2, m2);
+                            float2 y1 = fma2(make_float2(x[e + 2], x[e + 3]), c2, m2);
+                            y0.x = ex2(y0.x); y0.y = ex2(y0.y);
+                            y1.x = ex2(y1.x); y1.y = ex2(y1.y);
+                            sum0 = add2(sum0, y0);
+                            sum1 = add2(sum1, y1);
+                            u[i] = bf16_pair(y0.x, y0.y);
+                            u[i + 1] = bf16_pair(y1.x, y1.y);
+                        }
+                        tmem_st32(ts + h * 32, u);
+                    }
+                    sum0 = add2(sum0, sum1);
+                    l += sum0.x + sum0.y;
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                mbar_arrive_lane0(&p_full[s], lane);
+            }
+            if (!ok || !(ok = wait(&o_full[s], no_done, 3))) break;
+            ++no_done;
+            if (!warp_rows) continue;
+            tc_fence_after();
+            const bool real = r < ntok * a.G;
+            const int64_t row = ((int64_t)tok + rt) * a.hq + g * a.G + rh;
+            float z = l, f = 1.f, mm = m == -INFINITY ? 0.f : m;
+            if (!a.decode && a.off_by_one) {  // the added 1 is a logit of 0
+                const float top = fmaxf(mm, 0.f);
+                f = ex2(mm - top);
+                z = l * f + ex2(-top);
+                mm = top;
+            }
+            const float inv = z > 0.f ? f / z : (z == 0.f ? 0.f : z);  // NaN stays NaN
+            const float lse = (mm + log2f(z)) * kLn2;
+            const int64_t prow = (int64_t)slot * a.B * a.hq + row;
+            if (real) {
+                if (a.decode) a.plse[prow] = lse;
+                else if (a.lse) a.lse[row] = lse;
+            }
+#pragma unroll
+            for (int h = 0; h < D / 32; ++h) {
+                float y[32];
+                tmem_ld32(to + h * 32, y);
+                tmem_wait_ld();
+                if (real && a.decode) {
+                    float4 *p = reinterpret_cast<float4 *>(a.po + prow * D + h * 32);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        p[i] = make_float4(y[4 * i] * inv, y[4 * i + 1] * inv, y[4 * i + 2] * inv, y[4 * i + 3] * inv);
+                } else if (real) {
+                    uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row * D + h * 32);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        p[i] = make_uint4(bf16_pair(y[8 * i] * inv, y[8 * i + 1] * inv),
+                                          bf16_pair(y[8 * i + 2] * inv, y[8 * i + 3] * inv),
+                                          bf16_pair(y[8 * i + 4] * inv, y[8 * i + 5] * inv),
+                                          bf16_pair(y[8 * i + 6] * inv, y[8 * i + 7] * inv));
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const Args &a, int64_t items, int32_t *next, cudaStream_t st) {
+    CUtensorMap mq, mq1, mk[2], mv[2];
+    const uint64_t rows = (uint64_t)a.B * (a.decode ? 1 : a.L), tt = 128 / a.G;
+    bool ok = make_map3(&mq, a.q, D, a.hq, D, rows, (uint64_t)a.hq * D, a.G, (uint32_t)tt) &&
+              make_map3(&mq1, a.q, D, a.hq, D, rows, (uint64_t)a.hq * D, a.G, 1);
+    for (int i = 0; ok && i < 2; ++i) {
+        const uint64_t n = i ? a.cap : a.L, planes = i ? (uint64_t)a.B * a.hkv : (a.decode ? a.hkv : (uint64_t)a.B * a.hkv);
+        if (n == 0 || !a.k[i]) continue;
+        ok = make_map3(&mk[i], a.k[i], D, n, D, planes, a.plane[i], kKeys, 1) &&
+             make_map3(&mv[i], a.v[i], D, n, D, planes, a.plane[i], kKeys, 1);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    const bool have0 = a.L > 0, have1 = a.decode && a.cap > 0;
+    if (!have0) { mk[0] = mk[1]; mv[0] = mv[1]; }  // never read
+    if (!have1) { mk[1] = mk[0]; mv[1] = mv[0]; }
+    const size_t smem = Smem<D>::ALLOC;
+    cudaError_t e = set_smem_once((const void *)fwd_tc_kernel<D>, smem);
+    int dev = 0, sms = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int grid = (int)(items < sms ? items : sms);
+    fwd_tc_kernel<D><<<grid, kThreads, smem, st>>>(mq, mq1, mk[0], mv[0], mk[1], mv[1], a, next, wait_limit_ns());
+    return cudaGetLastError();
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn get_encode() {
+    static const EncodeTiledFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(p);
+        return EncodeTiledFn(nullptr);
+    }();
+    return fn;
+}
+
+}  // namespace
+
+bool tensor_maps_available() { return get_encode() != nullptr; }
+
+bool make_map3(CUtensorMap *m, const void *base, uint64_t cols, uint64_t n1, uint64_t s1, uint64_t n2, uint64_t s2,
+               uint32_t b1, uint32_t b2) {
+    EncodeTiledFn enc = get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {cols, n1, n2};
+    cuuint64_t strides[2] = {s1 * 2, s2 * 2};
+    cuuint32_t box[3] = {64, b1, b2};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_fwd_tc(const Args &a, int d, int64_t items, int32_t *next, cudaStream_t st) {
+    return d == 128 ? launch<128>(a, items, next, st) : launch<64>(a, items, next, st);
+}
+
+}  // namespace dense
+}  // namespace hsa
