@@ -181,14 +181,16 @@ __device__ __forceinline__ bool get_key_item(const BwdArgs &b, int i, int keys, 
     return it.nkeys > 0;
 }
 
-cudaError_t launch_fwd_simt(const Args &a, int d, bool bf16, int64_t max_items, cudaStream_t st);
+// fp32, on the CUDA cores (tiles of kSimtRows rows and keys)
+cudaError_t launch_fwd_simt(const Args &a, int d, int64_t items, cudaStream_t st);
 // bf16, on the tensor cores: a.tok is two row tiles (128 / G tokens each), but for a
 // decode call whose batch fits one; `next` is a zero int32, the items dealt so far.
 cudaError_t launch_fwd_tc(const Args &a, int d, int64_t items, int32_t *next, cudaStream_t st);
+// a.tok = 128 / G, key tiles of 128; `next`: two zero int32
+cudaError_t launch_bwd_tc(const BwdArgs &b, int d, int64_t row_items, int64_t key_items, int32_t *next, cudaStream_t st);
 cudaError_t launch_combine(const Args &a, int d, bool bf16, cudaStream_t st);
 cudaError_t launch_delta(const BwdArgs &b, int d, bool bf16, cudaStream_t st);
-cudaError_t launch_bwd_simt(const BwdArgs &b, int d, bool bf16, int64_t max_row_items, int64_t max_key_items,
-                            cudaStream_t st);
+cudaError_t launch_bwd_simt(const BwdArgs &b, int d, int64_t row_items, int64_t key_items, cudaStream_t st);
 
 }  // namespace dense
 }  // namespace hsa

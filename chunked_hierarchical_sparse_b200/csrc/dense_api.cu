@@ -69,14 +69,16 @@ int row_tile(const hsa_prompt_shape_t &s) {
     const int G = s.h_q / s.h_kv;
     return s.dtype == HSA_BF16 ? 2 * (128 / G) : kSimtRows / G;
 }
-int bwd_row_tile(const hsa_prompt_shape_t &s) { return kSimtRows / (s.h_q / s.h_kv); }
+// the backward's: one tile of rows, and its tiles of keys
+int bwd_row_tile(const hsa_prompt_shape_t &s) { return (s.dtype == HSA_BF16 ? 128 : kSimtRows) / (s.h_q / s.h_kv); }
+int bwd_key_tile(const hsa_prompt_shape_t &s) { return s.dtype == HSA_BF16 ? 128 : kSimtRows; }
 
 PromptWs carve_prompt(const hsa_prompt_shape_t &s, void *ws, bool bwd) {
     Carver c{static_cast<char *>(ws)};
     PromptWs w{};
     if (s.n_seq > 0) w.plan = c.take<int4>(plan_cap(s.L, s.n_seq, bwd ? bwd_row_tile(s) : row_tile(s)));
     if (bwd) {
-        if (s.n_seq > 0) w.kplan = c.take<int4>(plan_cap(s.L, s.n_seq, kSimtRows));
+        if (s.n_seq > 0) w.kplan = c.take<int4>(plan_cap(s.L, s.n_seq, bwd_key_tile(s)));
         w.delta = c.take<float>((size_t)s.B * s.L * s.h_q);
     }
     w.bytes = c.off;
@@ -196,7 +198,7 @@ hsa_status_t hsa_prompt_fwd(const hsa_prompt_shape_t *shape, const void *q, cons
     if (e == cudaSuccess) {
         const int64_t items = max_items(*shape, a.tok);
         e = shape->dtype == HSA_BF16 ? launch_fwd_tc(a, shape->d, items, word(ws, kWordNext), st)
-                                     : launch_fwd_simt(a, shape->d, false, items, st);
+                                     : launch_fwd_simt(a, shape->d, items, st);
     }
     return cuda_status(e);
 }
@@ -217,18 +219,21 @@ hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, cons
     b.a = prompt_args(*shape, q, k, v, ws, w, bwd_row_tile(*shape));
     b.kplan = w.kplan;
     b.kplan_n = word(ws, kWordKPlanN);
-    b.ktiles = (int)ceil_div(shape->L, kSimtRows);
+    b.ktiles = (int)ceil_div(shape->L, bwd_key_tile(*shape));
     b.o = o; b.dO = dO; b.lse = lse; b.delta = w.delta;
     b.dq = dq; b.dk = dk; b.dv = dv;
     TimedLaunch tl(HSA_K_PROMPT_BWD, cu_seqlens ? 5 : 3, st);
     if (cu_seqlens) {
         e = launch_plan(cu_seqlens, shape->n_seq, shape->L, b.a.tok, false, w.plan, word(ws, kWordPlanN), b.a.ds, st);
         if (e == cudaSuccess)
-            e = launch_plan(cu_seqlens, shape->n_seq, shape->L, kSimtRows, true, w.kplan, word(ws, kWordKPlanN), b.a.ds, st);
+            e = launch_plan(cu_seqlens, shape->n_seq, shape->L, bwd_key_tile(*shape), true, w.kplan, word(ws, kWordKPlanN), b.a.ds, st);
     }
     if (e == cudaSuccess) e = launch_delta(b, shape->d, bf16, st);
-    if (e == cudaSuccess)
-        e = launch_bwd_simt(b, shape->d, bf16, max_items(*shape, b.a.tok), max_items(*shape, kSimtRows), st);
+    if (e == cudaSuccess) {
+        const int64_t row_items = max_items(*shape, b.a.tok), key_items = max_items(*shape, bwd_key_tile(*shape));
+        e = bf16 ? launch_bwd_tc(b, shape->d, row_items, key_items, word(ws, kWordNext), st)
+                 : launch_bwd_simt(b, shape->d, row_items, key_items, st);
+    }
     return cuda_status(e);
 }
 
@@ -275,7 +280,7 @@ hsa_status_t hsa_prefix_decode(const hsa_prefix_shape_t *shape, const void *q, c
     TimedLaunch tl(HSA_K_PREFIX, items > 0 ? 2 : 1, st);
     if (items > 0)
         e = bf16 ? launch_fwd_tc(a, shape->d, items, word(ws, kWordNext), st)
-                 : launch_fwd_simt(a, shape->d, false, items, st);
+                 : launch_fwd_simt(a, shape->d, items, st);
     if (e == cudaSuccess) e = launch_combine(a, shape->d, bf16, st);
     return cuda_status(e);
 }

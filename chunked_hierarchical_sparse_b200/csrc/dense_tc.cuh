@@ -50,21 +50,23 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 }
 
 // Converged wait of a warp for phase `parity` of `bar`; false once it ran out (the
-// first to run out sets *abort and reports) or another role gave up.
+// first to run out sets *abort and reports) or another role gave up.  A limit below
+// the timer's resolution (about 1 us) runs out at once: try_wait alone may sleep longer.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns, volatile int *abort,
                                           DevStatus *ds, int role) {
-    bool ok = mbar_try(bar, parity);
+    const bool at_once = limit_ns < 1000;
+    bool ok = at_once ? mbar_test(bar, parity) : mbar_try(bar, parity);
     if (!__all_sync(0xffffffffu, ok)) {
         const uint64_t t0 = globaltimer();
         while (true) {
-            ok = mbar_try(bar, parity);
-            if (__all_sync(0xffffffffu, ok)) break;
             if (__any_sync(0xffffffffu, *abort != 0)) return false;
-            if (__any_sync(0xffffffffu, globaltimer() - t0 > limit_ns)) {
+            if (__any_sync(0xffffffffu, at_once || globaltimer() - t0 > limit_ns)) {
                 *abort = 1;
                 report(ds, HSA_ERR_TIMEOUT, kKDense, role, 0);
                 return false;
             }
+            ok = mbar_try(bar, parity);
+            if (__all_sync(0xffffffffu, ok)) break;
         }
     }
     return true;

@@ -1,0 +1,668 @@
+// k_dense_bwd_tc.cu -- backward of the dense prompt pass on the tensor cores (bf16).
+//
+// Mathematics.  With p = 2^(S c - lse log2 e) (S = Q K^T, c = log2(e)/sqrt(d)),
+// dP = dO V^T and D = rowsum(dO o):  dS = p (dP - D),  dV = p^T dO,
+// dK = dS^T Q / sqrt(d),  dQ = dS K / sqrt(d).
+//
+// Two passes over the tile pairs, one per stationary operand, instead of one that
+// adds dQ tiles into memory: 7 products instead of 5, but no fp32 dQ in memory, no
+// atomics (the result does not depend on timing) and nothing but plain stores.
+// (Adding 64 KB of fp32 per 128 x 128 tile pair at the 4.8 TB/s that vector
+// reductions reach on this GPU takes 2 us per SM, as long as the five products.)
+// Both keep every first operand of a second product in tensor memory:
+// - key pass: 128 keys per CTA, walking the row tiles that see them.  S^T = K Q^T
+//   and dP^T = V dO^T have a key per tensor-memory lane; p and dS go back over them
+//   as bf16 and feed dV += p dO, dK += dS Q directly.  The group's heads are rows
+//   of the same tiles, so dK and dV of shared heads are summed by the products.
+// - row pass: 128 (token, head) rows per CTA, walking the keys: S, dP, then
+//   dQ += dS K.  S has two buffers, so the tensor cores run ahead of the exponentials.
+// Two compute warpgroups take half of a tile's columns each (64 values of S and of dP
+// per thread); the MMAs are issued so that one warpgroup step always has one or two
+// products running behind it.
+#include "dense_tc.cuh"
+
+namespace hsa {
+namespace dense {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTile = 128;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpStat = 10;
+constexpr int kItems = 2;
+
+template <int D, bool KEYS> struct Smem {
+    static constexpr int NH = D / 64;
+    static constexpr int TILE = NH * 128 * 128;           // bytes of a 128 x D bf16 tile
+    static constexpr int ST = KEYS ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);
+    static constexpr int OFF_FIX = 0;                     // the two stationary tiles
+    static constexpr int OFF_RING = 2 * TILE;
+    static constexpr int OFF_STAT = OFF_RING + ST * TILE; // key pass: [2][lse, delta][128]
+    static constexpr int OFF_ITEM = OFF_STAT + (KEYS ? 2048 : 0);
+    static constexpr int OFF_BAR = OFF_ITEM + kItems * 64;
+    static constexpr int OFF_MISC = OFF_BAR + 512;
+    static constexpr int ALLOC = OFF_MISC + 64 + 1024;    // + alignment to 1 KB
+};
+static_assert(Smem<128, true>::ALLOC <= 232448 && Smem<128, false>::ALLOC <= 232448, "shared memory of a CTA");
+
+// rows [r0, 128) of a swizzled tile set to zero by one warp, before MMAs read it
+template <int NH> __device__ __forceinline__ void clear_rows(uint8_t *tile, int r0, int lane) {
+    for (int i = r0 * 8 + lane; i < kTile * 8; i += 32)
+#pragma unroll
+        for (int h = 0; h < NH; ++h) *reinterpret_cast<uint4 *>(tile + h * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// D[128 x 128] = A B^T over d, both tiles K-major in shared memory
+template <int D> __device__ __forceinline__ void mma_dots(uint32_t dst, uint32_t a, uint32_t b) {
+    constexpr uint32_t id = idesc_bf16_f32(128, kTile, false, false);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+        mma_bf16_ss(dst, smem_desc_sw128(a + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                    smem_desc_sw128(b + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), id, ks > 0);
+}
+// D[128 x d] (+)= A B, A in tensor memory (the two warpgroups' halves, 64 of the 128
+// contracted indices each, 64 columns apart), B a tile with the contracted index as its rows
+template <int D> __device__ __forceinline__ void mma_sum(uint32_t dst, uint32_t a, uint32_t b, bool add) {
+    constexpr uint32_t id = idesc_bf16_f32(128, D, false, true);
+#pragma unroll
+    for (int ks = 0; ks < kTile / 16; ++ks)
+        mma_bf16_ts(dst, a + (ks >> 2) * 64 + (ks & 3) * 8, smem_desc_sw128(b + ks * 2048, 16384, 1024), id, add || ks > 0);
+}
+
+__device__ __forceinline__ void load64(uint32_t t, float (&x)[64]) {
+    float(&x0)[32] = *reinterpret_cast<float(*)[32]>(x);
+    float(&x1)[32] = *reinterpret_cast<float(*)[32]>(x + 32);
+    tmem_ld32(t, x0);
+    tmem_ld32(t + 32, x1);
+    tmem_wait_ld();
+}
+__device__ __forceinline__ void store64(uint32_t t, const float (&x)[64]) {  // as 32 bf16 pairs
+    uint32_t u[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) u[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+    tmem_st32(t, u);
+    tmem_wait_st();
+}
+// one row of a [128 x d] accumulator, scaled, to global memory
+template <int D> __device__ __forceinline__ void store_row(uint32_t t, float f, __nv_bfloat16 *dst, bool real) {
+#pragma unroll
+    for (int h = 0; h < D / 32; ++h) {
+        float y[32];
+        tmem_ld32(t + h * 32, y);
+        tmem_wait_ld();
+        if (real) {
+            uint4 *p = reinterpret_cast<uint4 *>(dst + h * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                p[i] = make_uint4(bf16_pair(y[8 * i] * f, y[8 * i + 1] * f), bf16_pair(y[8 * i + 2] * f, y[8 * i + 3] * f),
+                                  bf16_pair(y[8 * i + 4] * f, y[8 * i + 5] * f), bf16_pair(y[8 * i + 6] * f, y[8 * i + 7] * f));
+        }
+        __syncwarp();
+    }
+}
+
+struct BwdItem {
+    int end, g, plane;
+    int tok0, ntok;    // row pass: first token row and tokens; key pass: the sequence's first token row, its length
+    int key0, nkeys;   // first key row (inside its plane) and keys
+    int off;           // row pass: causal offset; key pass: first key's index in the sequence
+    int foreign, pad[7];
+};
+static_assert(sizeof(BwdItem) == 64, "item ring");
+
+// ---------------------------------------------------------------------- key pass
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const __grid_constant__ BwdArgs b, int32_t *next, uint64_t wait_ns) {
+    using L = Smem<D, true>;
+    const Args &a = b.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *stat = reinterpret_cast<float *>(sm + L::OFF_STAT);
+    BwdItem *items = reinterpret_cast<BwdItem *>(sm + L::OFF_ITEM);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
+    uint64_t *item_full = bar, *item_empty = bar + 2, *fix_full = bar + 4, *fix_empty = bar + 5;
+    uint64_t *stat_full = bar + 6, *stat_empty = bar + 8;
+    uint64_t *s_full = bar + 10, *dp_full = bar + 11, *p_full = bar + 12, *ds_full = bar + 13, *acc_full = bar + 14;
+    uint64_t *done = bar + 15, *ring_full = bar + 16, *ring_empty = ring_full + L::ST;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tt = 128 / a.G, rows = tt * a.G;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 10);
+            mbar_init(&stat_full[i], 1); mbar_init(&stat_empty[i], 8);
+        }
+        mbar_init(fix_full, 1); mbar_init(fix_empty, 1);
+        mbar_init(s_full, 1); mbar_init(dp_full, 1); mbar_init(p_full, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
+        mbar_init(done, 1);
+        for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    // rows that no box writes (G does not divide 128) take part in the sums over rows: zeros
+    if (rows < 128) {
+        for (int i = threadIdx.x; i < L::ST * L::TILE / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(sm + L::OFF_RING)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == kWarpLoad && lane == 0) {
+        prefetch_tmap(&tm_q); prefetch_tmap(&tm_do); prefetch_tmap(&tm_k); prefetch_tmap(&tm_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + D;
+    auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
+    // row tiles of an item: from the one that holds its first key's token to the sequence's end
+    auto first_tile = [&](const BwdItem &t) { return t.off / tt; };
+    auto end_tile = [&](const BwdItem &t) { return (t.ntok + tt - 1) / tt; };
+
+    if (warp == kWarpLoad) {
+        // ============================================================ items and loads
+        const int total = key_item_count(b);
+        int idx = blockIdx.x, pos = 0, fixes = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            BwdItem t{};
+            KeyItem it;
+            t.end = idx >= total || !get_key_item(b, idx, kTile, it);
+            if (!t.end) {
+                t.g = it.g; t.plane = it.plane; t.tok0 = (int)it.row0; t.ntok = it.len;
+                t.key0 = it.start + it.n0; t.nkeys = it.nkeys; t.off = it.n0;
+            }
+            const int ib = n % kItems;
+            if (n >= kItems && !(ok = wait(&item_empty[ib], n / kItems - 1, 11))) break;
+            if (lane == 0) {
+                items[ib] = t;
+                mbar_arrive(&item_full[ib]);
+            }
+            __syncwarp();
+            if (t.end) break;
+            if (n > 0 && !(ok = wait(fix_empty, n - 1, 11))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(fix_full, 2 * L::TILE);
+#pragma unroll
+                for (int h = 0; h < L::NH; ++h) {
+                    tma_load_3d(sm + L::OFF_FIX + h * 16384, &tm_k, h * 64, t.key0, t.plane, fix_full);
+                    tma_load_3d(sm + L::OFF_FIX + L::TILE + h * 16384, &tm_v, h * 64, t.key0, t.plane, fix_full);
+                }
+            }
+            ++fixes;
+            const int j1 = end_tile(t);
+            for (int j = first_tile(t); ok && j < j1; ++j) {
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const int st = pos % L::ST;
+                    if (pos >= L::ST && !(ok = wait(&ring_empty[st], pos / L::ST - 1, 11))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&ring_full[st], L::NH * rows * 128);
+#pragma unroll
+                        for (int h = 0; h < L::NH; ++h)
+                            tma_load_3d(sm + L::OFF_RING + st * L::TILE + h * 16384, o ? &tm_do : &tm_q, h * 64, t.g * a.G,
+                                        t.tok0 + j * tt, &ring_full[st]);
+                    }
+                    ++pos;
+                }
+            }
+            int i = 0;
+            if (lane == 0) i = atomicAdd(next, 1);
+            idx = __shfl_sync(0xffffffffu, i, 0) + gridDim.x;
+        }
+        if (!ok && lane == 0) {  // the loads in flight land before the CTA goes away (bounded)
+            for (int i = max(0, pos - L::ST); i < pos; ++i) mbar_wait(&ring_full[i % L::ST], (i / L::ST) & 1, kDrainWaitNs);
+            if (fixes) mbar_wait(fix_full, (fixes - 1) & 1, kDrainWaitNs);
+        }
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        // ============================================================ MMA issue
+        int pos = 0, np = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const int ib = n % kItems;
+            if (!(ok = wait(&item_full[ib], n / kItems, 12))) break;
+            const BwdItem t = items[ib];
+            __syncwarp();
+            mbar_arrive_lane0(&item_empty[ib], lane);
+            if (t.end) break;
+            if (!(ok = wait(fix_full, n, 12))) break;
+            const uint32_t kb = smem_u32(sm + L::OFF_FIX), vb = kb + L::TILE;
+            const int j0 = first_tile(t), j1 = end_tile(t);
+            auto ring = [&](int p) { return smem_u32(sm + L::OFF_RING + (p % L::ST) * L::TILE); };
+            // tile j's Q (o = 0) or dO (o = 1) is in shared memory; rows behind the sequence's last
+            // token are another's (or nothing's): cleared, since the sums run over all 128 rows
+            auto ready = [&](int p, int j) -> bool {
+                if (!wait(&ring_full[p % L::ST], p / L::ST, 12)) return false;
+                const int real = (t.ntok - j * tt) * a.G;
+                if (real < rows) {
+                    clear_rows<L::NH>(sm + L::OFF_RING + (p % L::ST) * L::TILE, real, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                return true;
+            };
+            if (!(ok = ready(pos, j0))) break;
+            if (lane == 0) { tc_fence_after(); mma_dots<D>(t_s, kb, ring(pos)); mma_commit(s_full); }
+            if (!(ok = ready(pos + 1, j0))) break;
+            if (lane == 0) { mma_dots<D>(t_dp, vb, ring(pos + 1)); mma_commit(dp_full); }
+            for (int j = j0; j < j1; ++j) {
+                const int pq = pos, pd = pos + 1;
+                const bool more = j + 1 < j1;
+                if (!(ok = wait(p_full, np, 12))) break;
+                if (lane == 0) {
+                    tc_fence_after();
+                    mma_sum<D>(t_dv, t_s, ring(pd), j > j0);
+                    mma_commit(&ring_empty[pd % L::ST]);
+                }
+                if (more) {
+                    if (!(ok = ready(pos + 2, j + 1))) break;
+                    if (lane == 0) { tc_fence_after(); mma_dots<D>(t_s, kb, ring(pos + 2)); mma_commit(s_full); }
+                }
+                if (!(ok = wait(ds_full, np, 12))) break;
+                ++np;
+                if (lane == 0) {
+                    tc_fence_after();
+                    mma_sum<D>(t_dk, t_dp, ring(pq), j > j0);
+                    mma_commit(&ring_empty[pq % L::ST]);
+                    if (!more) { mma_commit(acc_full); mma_commit(fix_empty); }
+                }
+                if (more) {
+                    if (!(ok = ready(pos + 3, j + 1))) break;
+                    if (lane == 0) { tc_fence_after(); mma_dots<D>(t_dp, vb, ring(pos + 3)); mma_commit(dp_full); }
+                }
+                pos += 2;
+            }
+        }
+        if (!ok && lane == 0) {  // the MMAs issued so far end before tensor memory is freed (bounded)
+            mma_commit(done);
+            mbar_wait(done, 0, kDrainWaitNs);
+        }
+        __syncwarp();
+    } else if (warp == kWarpStat) {
+        // ============================================================ row statistics of each tile
+        int nt = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const int ib = n % kItems;
+            if (!(ok = wait(&item_full[ib], n / kItems, 13))) break;
+            const BwdItem t = items[ib];
+            __syncwarp();
+            mbar_arrive_lane0(&item_empty[ib], lane);
+            if (t.end) break;
+            const int j1 = end_tile(t);
+            for (int j = first_tile(t); j < j1; ++j, ++nt) {
+                float l2[4], de[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = i * 32 + lane, tk = j * tt + r / a.G;
+                    const bool real = r < rows && tk < t.ntok;
+                    const int64_t at = ((int64_t)t.tok0 + tk) * a.hq + t.g * a.G + r % a.G;
+                    l2[i] = real ? b.lse[at] * kLog2e : INFINITY;  // p = 2^-inf = 0
+                    de[i] = real ? b.delta[at] : 0.f;
+                }
+                if (nt >= 2 && !(ok = wait(&stat_empty[nt & 1], (nt >> 1) - 1, 13))) break;
+                float *s = stat + (nt & 1) * 256;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[i * 32 + lane] = l2[i];
+                    s[128 + i * 32 + lane] = de[i];
+                }
+                __syncwarp();
+                mbar_arrive_lane0(&stat_full[nt & 1], lane);
+            }
+        }
+    } else if (warp < 8) {
+        // ============================================================ p and dS, 64 columns per warpgroup
+        const int w = warp >> 2, key = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t xs = t_s + lanes + w * 64, xd = t_dp + lanes + w * 64;
+        const float c = a.scale_log2;
+        int nt = 0, na = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const int ib = n % kItems;
+            if (!(ok = wait(&item_full[ib], n / kItems, 14))) break;
+            const BwdItem t = items[ib];
+            __syncwarp();
+            mbar_arrive_lane0(&item_empty[ib], lane);
+            if (t.end) break;
+            const int j1 = end_tile(t);
+            for (int j = first_tile(t); j < j1; ++j, ++nt) {
+                const float4 *s4 = reinterpret_cast<const float4 *>(stat + (nt & 1) * 256 + w * 64);
+                if (!(ok = wait(&stat_full[nt & 1], nt >> 1, 14))) break;
+                if (!(ok = wait(s_full, nt, 14))) break;
+                tc_fence_after();
+                float x[64];
+                load64(xs, x);
+                const float2 c2 = make_float2(c, c);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 l = s4[i];
+                    const float2 u = fma2(make_float2(x[4 * i], x[4 * i + 1]), c2, make_float2(-l.x, -l.y));
+                    const float2 v = fma2(make_float2(x[4 * i + 2], x[4 * i + 3]), c2, make_float2(-l.z, -l.w));
+                    x[4 * i] = ex2(u.x); x[4 * i + 1] = ex2(u.y); x[4 * i + 2] = ex2(v.x); x[4 * i + 3] = ex2(v.y);
+                }
+                if (j * tt < t.off + kTile - 1) {  // some row of the tile does not see some of the keys
+                    const int first = (t.off + key - j * tt) * a.G - w * 64;  // first column that sees this key
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) x[i] = i >= first ? x[i] : 0.f;
+                }
+                store64(xs, x);
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_lane0(p_full, lane);
+                if (!(ok = wait(dp_full, nt, 14))) break;
+                tc_fence_after();
+                float y[64];
+                load64(xd, y);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 d = s4[32 + i];
+                    const float2 u = mul2(make_float2(x[4 * i], x[4 * i + 1]), add2(make_float2(y[4 * i], y[4 * i + 1]), make_float2(-d.x, -d.y)));
+                    const float2 v = mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), add2(make_float2(y[4 * i + 2], y[4 * i + 3]), make_float2(-d.z, -d.w)));
+                    x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = v.x; x[4 * i + 3] = v.y;
+                }
+                store64(xd, x);
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_lane0(ds_full, lane);
+                mbar_arrive_lane0(&stat_empty[nt & 1], lane);
+            }
+            if (!ok || !(ok = wait(acc_full, na, 14))) break;
+            ++na;
+            tc_fence_after();
+            const int64_t at = (int64_t)t.plane * a.plane[0] + (int64_t)(t.key0 + key) * D;
+            if (w == 0) store_row<D>(t_dv + lanes, 1.f, static_cast<__nv_bfloat16 *>(b.dv) + at, key < t.nkeys);
+            else store_row<D>(t_dk + lanes, a.scale, static_cast<__nv_bfloat16 *>(b.dk) + at, key < t.nkeys);
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------- row pass
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const __grid_constant__ BwdArgs b, int32_t *next, uint64_t wait_ns) {
+    using L = Smem<D, false>;
+    const Args &a = b.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    BwdItem *items = reinterpret_cast<BwdItem *>(sm + L::OFF_ITEM);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
+    uint64_t *item_full = bar, *item_empty = bar + 2, *fix_full = bar + 4, *fix_empty = bar + 5;
+    uint64_t *s_full = bar + 6, *dp_full = bar + 8, *dp_read = bar + 9, *ds_full = bar + 10, *acc_full = bar + 11;
+    uint64_t *done = bar + 12, *ring_full = bar + 13, *ring_empty = ring_full + L::ST;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tt = 128 / a.G, rows = tt * a.G;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 9); mbar_init(&s_full[i], 1); }
+        mbar_init(fix_full, 1); mbar_init(fix_empty, 1);
+        mbar_init(dp_full, 1); mbar_init(dp_read, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
+        mbar_init(done, 1);
+        for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == kWarpLoad && lane == 0) {
+        prefetch_tmap(&tm_q); prefetch_tmap(&tm_do); prefetch_tmap(&tm_k); prefetch_tmap(&tm_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;  // S: two buffers
+    auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
+    auto tiles = [](int keys) { return (keys + kTile - 1) / kTile; };
+
+    if (warp == kWarpLoad) {
+        // ============================================================ items and loads
+        const int total = item_count(a);
+        int idx = blockIdx.x, pos = 0, fixes = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            BwdItem t{};
+            Item it;
+            t.end = idx >= total || !get_item(a, idx, it);
+            if (!t.end) {
+                t.g = it.g; t.plane = it.plane; t.tok0 = it.tok0; t.ntok = it.ntok;
+                t.key0 = it.key0; t.nkeys = it.nkeys; t.off = it.off; t.foreign = it.foreign;
+            }
+            const int ib = n % kItems;
+            if (n >= kItems && !(ok = wait(&item_empty[ib], n / kItems - 1, 21))) break;
+            if (lane == 0) {
+                items[ib] = t;
+                mbar_arrive(&item_full[ib]);
+            }
+            __syncwarp();
+            if (t.end) break;
+            if (n > 0 && !(ok = wait(fix_empty, n - 1, 21))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(fix_full, 2 * L::NH * rows * 128);
+#pragma unroll
+                for (int h = 0; h < L::NH; ++h) {
+                    tma_load_3d(sm + L::OFF_FIX + h * 16384, &tm_q, h * 64, t.g * a.G, t.tok0, fix_full);
+                    tma_load_3d(sm + L::OFF_FIX + L::TILE + h * 16384, &tm_do, h * 64, t.g * a.G, t.tok0, fix_full);
+                }
+            }
+            ++fixes;
+            const int nt = tiles(t.nkeys);
+            for (int j = 0; ok && j < nt; ++j) {
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const int st = pos % L::ST;
+                    if (pos >= L::ST && !(ok = wait(&ring_empty[st], pos / L::ST - 1, 21))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&ring_full[st], L::TILE);
+#pragma unroll
+                        for (int h = 0; h < L::NH; ++h)
+                            tma_load_3d(sm + L::OFF_RING + st * L::TILE + h * 16384, o ? &tm_v : &tm_k, h * 64,
+                                        t.key0 + j * kTile, t.plane, &ring_full[st]);
+                    }
+                    ++pos;
+                }
+            }
+            int i = 0;
+            if (lane == 0) i = atomicAdd(next, 1);
+            idx = __shfl_sync(0xffffffffu, i, 0) + gridDim.x;
+        }
+        if (!ok && lane == 0) {
+            for (int i = max(0, pos - L::ST); i < pos; ++i) mbar_wait(&ring_full[i % L::ST], (i / L::ST) & 1, kDrainWaitNs);
+            if (fixes) mbar_wait(fix_full, (fixes - 1) & 1, kDrainWaitNs);
+        }
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        // ============================================================ MMA issue
+        int pos = 0, nt = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const int ib = n % kItems;
+            if (!(ok = wait(&item_full[ib], n / kItems, 22))) break;
+            const BwdItem t = items[ib];
+            __syncwarp();
+            mbar_arrive_lane0(&item_empty[ib], lane);
+            if (t.end) break;
+            if (!(ok = wait(fix_full, n, 22))) break;
+            const uint32_t qb = smem_u32(sm + L::OFF_FIX), ob = qb + L::TILE;
+            const int nn = tiles(t.nkeys);
+            auto ring = [&](int p) { return smem_u32(sm + L::OFF_RING + (p % L::ST) * L::TILE); };
+            auto scores = [&](int j) -> bool {  // S of key tile j, into buffer nt & 1 of that tile
+                const int p = pos + 2 * j;
+                if (!wait(&ring_full[p % L::ST], p / L::ST, 22)) return false;
+                if (t.foreign && j == nn - 1) {  // dS is 0 there, but 0 * NaN is not
+                    clear_rows<L::NH>(sm + L::OFF_RING + (p % L::ST) * L::TILE, t.nkeys - j * kTile, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    tc_fence_after();
+                    const int sb = (nt + j) & 1;
+                    mma_dots<D>(t_s + sb * 128, qb, ring(p));
+                    mma_commit(&s_full[sb]);
+                }
+                return true;
+            };
+            auto dprob = [&](int j) -> bool {
+                const int p = pos + 2 * j + 1;
+                if (!wait(&ring_full[p % L::ST], p / L::ST, 22)) return false;
+                if (lane == 0) {
+                    tc_fence_after();
+                    mma_dots<D>(t_dp, ob, ring(p));
+                    mma_commit(dp_full);
+                    mma_commit(&ring_empty[p % L::ST]);
+                    if (j == nn - 1) mma_commit(fix_empty);
+                }
+                return true;
+            };
+            ok = scores(0) && dprob(0);
+            for (int j = 0; ok && j < nn; ++j) {
+                if (j + 1 < nn) {
+                    if (!(ok = scores(j + 1))) break;
+                    if (!(ok = wait(dp_read, nt + j, 22))) break;
+                    if (!(ok = dprob(j + 1))) break;
+                } else if (!(ok = wait(dp_read, nt + j, 22))) {
+                    break;
+                }
+                if (!(ok = wait(ds_full, nt + j, 22))) break;
+                if (lane == 0) {
+                    tc_fence_after();
+                    const int p = pos + 2 * j;
+                    mma_sum<D>(t_dq, t_s + ((nt + j) & 1) * 128, ring(p), j > 0);
+                    mma_commit(&ring_empty[p % L::ST]);
+                    if (j == nn - 1) mma_commit(acc_full);
+                }
+            }
+            pos += 2 * nn;
+            nt += nn;
+        }
+        if (!ok && lane == 0) {
+            mma_commit(done);
+            mbar_wait(done, 0, kDrainWaitNs);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ============================================================ dS, 64 keys per warpgroup
+        const int w = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t xd = t_dp + lanes + w * 64;
+        const float c = a.scale_log2;
+        const int rt = r / a.G, rh = r % a.G;
+        int nt = 0, na = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const int ib = n % kItems;
+            if (!(ok = wait(&item_full[ib], n / kItems, 24))) break;
+            const BwdItem t = items[ib];
+            __syncwarp();
+            mbar_arrive_lane0(&item_empty[ib], lane);
+            if (t.end) break;
+            const bool real = r < t.ntok * a.G;
+            const int64_t row = ((int64_t)t.tok0 + rt) * a.hq + t.g * a.G + rh;
+            const float l2 = real ? b.lse[row] * kLog2e : INFINITY, de = real ? b.delta[row] : 0.f;
+            const int lim = min(t.nkeys - 1, t.off + rt), lim_all = min(t.nkeys - 1, t.off);
+            const int nn = tiles(t.nkeys);
+            for (int j = 0; j < nn; ++j, ++nt) {
+                const int sb = nt & 1;
+                const uint32_t xs = t_s + lanes + sb * 128 + w * 64;
+                if (!(ok = wait(&s_full[sb], nt >> 1, 24))) break;
+                tc_fence_after();
+                float x[64];
+                load64(xs, x);
+                const float2 c2 = make_float2(c, c), m2 = make_float2(-l2, -l2);
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    const float2 u = fma2(make_float2(x[i], x[i + 1]), c2, m2);
+                    x[i] = ex2(u.x);
+                    x[i + 1] = ex2(u.y);
+                }
+                if (!(ok = wait(dp_full, nt, 24))) break;
+                tc_fence_after();
+                float y[64];
+                load64(xd, y);
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_lane0(dp_read, lane);
+                const float2 d2 = make_float2(-de, -de);
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    const float2 u = mul2(make_float2(x[i], x[i + 1]), add2(make_float2(y[i], y[i + 1]), d2));
+                    x[i] = u.x;
+                    x[i + 1] = u.y;
+                }
+                if (j * kTile + kTile - 1 > lim_all) {
+                    const int last = lim - j * kTile - w * 64;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) x[i] = i <= last ? x[i] : 0.f;
+                }
+                store64(xs, x);
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_lane0(ds_full, lane);
+            }
+            if (!ok || !(ok = wait(acc_full, na, 24))) break;
+            ++na;
+            tc_fence_after();
+            // each warpgroup stores half of the row
+            store_row<D / 2>(t_dq + lanes + w * (D / 2), a.scale, static_cast<__nv_bfloat16 *>(b.dq) + row * D + w * (D / 2), real);
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const BwdArgs &b, int64_t row_items, int64_t key_items, int32_t *next, cudaStream_t st) {
+    const Args &a = b.a;
+    CUtensorMap mq, mo, mk, mv;
+    const uint64_t toks = (uint64_t)a.B * a.L, tt = 128 / a.G, planes = (uint64_t)a.B * a.hkv;
+    if (!make_map3(&mq, a.q, D, a.hq, D, toks, (uint64_t)a.hq * D, a.G, (uint32_t)tt) ||
+        !make_map3(&mo, b.dO, D, a.hq, D, toks, (uint64_t)a.hq * D, a.G, (uint32_t)tt) ||
+        !make_map3(&mk, a.k[0], D, a.L, D, planes, a.plane[0], kTile, 1) ||
+        !make_map3(&mv, a.v[0], D, a.L, D, planes, a.plane[0], kTile, 1))
+        return cudaErrorInvalidValue;
+    cudaError_t e = set_smem_once((const void *)bwd_key_tc_kernel<D>, Smem<D, true>::ALLOC);
+    if (e == cudaSuccess) e = set_smem_once((const void *)bwd_row_tc_kernel<D>, Smem<D, false>::ALLOC);
+    int dev = 0, sms = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    bwd_key_tc_kernel<D><<<(int)(key_items < sms ? key_items : sms), kThreads, Smem<D, true>::ALLOC, st>>>(
+        mq, mo, mk, mv, b, next, wait_limit_ns());
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    bwd_row_tc_kernel<D><<<(int)(row_items < sms ? row_items : sms), kThreads, Smem<D, false>::ALLOC, st>>>(
+        mq, mo, mk, mv, b, next + 1, wait_limit_ns());
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_tc(const BwdArgs &b, int d, int64_t row_items, int64_t key_items, int32_t *next, cudaStream_t st) {
+    return d == 128 ? launch<128>(b, row_items, key_items, next, st) : launch<64>(b, row_items, key_items, next, st);
+}
+
+}  // namespace dense
+}  // namespace hsa

@@ -369,8 +369,7 @@ template <typename T, int D> cudaError_t bwd(const BwdArgs &b, int64_t row_items
 
 }  // namespace
 
-cudaError_t launch_fwd_simt(const Args &a, int d, bool bf16, int64_t items, cudaStream_t st) {
-    if (bf16) return d == 128 ? fwd<__nv_bfloat16, 128>(a, items, st) : fwd<__nv_bfloat16, 64>(a, items, st);
+cudaError_t launch_fwd_simt(const Args &a, int d, int64_t items, cudaStream_t st) {
     return d == 128 ? fwd<float, 128>(a, items, st) : fwd<float, 64>(a, items, st);
 }
 
@@ -379,10 +378,7 @@ cudaError_t launch_delta(const BwdArgs &b, int d, bool bf16, cudaStream_t st) {
     return d == 128 ? delta<float, 128>(b, st) : delta<float, 64>(b, st);
 }
 
-cudaError_t launch_bwd_simt(const BwdArgs &b, int d, bool bf16, int64_t row_items, int64_t key_items, cudaStream_t st) {
-    if (bf16)
-        return d == 128 ? bwd<__nv_bfloat16, 128>(b, row_items, key_items, st)
-                        : bwd<__nv_bfloat16, 64>(b, row_items, key_items, st);
+cudaError_t launch_bwd_simt(const BwdArgs &b, int d, int64_t row_items, int64_t key_items, cudaStream_t st) {
     return d == 128 ? bwd<float, 128>(b, row_items, key_items, st) : bwd<float, 64>(b, row_items, key_items, st);
 }
 

@@ -200,6 +200,32 @@ def test_prompt_bad_bounds_are_reported(bad, dtype):
         assert all((t == MARK).all() for t in b.values())
 
 
+def test_waits_that_run_out_are_reported():
+    """Every wait bounded by 1 ns: a timeout in the status word, a usable device, a clean next call."""
+    m = hsa()
+    x = inputs(1, 700, 16, 2, 128, "bf16", seed=21)
+    good = run_prompt(x)
+    dx = decode_inputs(5, 900, 300, 16, 2, 128, "bf16", [300, 1, 0, 77, 128], seed=22)
+    gd = run_decode(dx)
+    m.hsa_set_wait_limit_ns(1)
+    try:
+        codes = []
+        b = {n: t.clone() for n, t in good.items()}
+        ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+        m.hsa_prompt_fwd(x["q"], x["k"], x["v"], o=b["o"], ws=ws)
+        codes.append(m.hsa_device_status(ws))
+        m.hsa_prompt_bwd(x["q"], x["k"], x["v"], good["o"], x["dO"], good["lse"], ws=ws)
+        codes.append(m.hsa_device_status(ws))
+        m.hsa_prefix_decode(dx["q"], dx["kp"], dx["vp"], dx["kc"], dx["vc"], dx["lens"], ws=ws)
+        codes.append(m.hsa_device_status(ws))
+    finally:
+        m.hsa_set_wait_limit_ns(0)
+    assert codes == [5, 5, 5]
+    again = run_prompt(x)
+    assert all(torch.equal(good[n], again[n]) for n in good)
+    assert torch.equal(gd["o"], run_decode(dx)["o"])
+
+
 def test_prompt_empty():
     m = hsa()
     for B, L in ((0, 5), (2, 0)):
