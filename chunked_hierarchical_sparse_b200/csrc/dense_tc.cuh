@@ -72,6 +72,122 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64
     return true;
 }
 
+// The same for a role that a single thread plays: no votes, the shortest path from a
+// barrier to the next instruction (a converged wait costs the issuing warp about 100
+// cycles even when the phase is long complete).
+__device__ __forceinline__ bool thread_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns, volatile int *abort,
+                                            DevStatus *ds, int role) {
+    const bool at_once = limit_ns < 1000;
+    if (at_once ? mbar_test(bar, parity) : mbar_try(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    while (true) {
+        if (*abort) return false;
+        if (at_once || globaltimer() - t0 > limit_ns) {
+            *abort = 1;
+            report(ds, HSA_ERR_TIMEOUT, kKDense, role, 0);
+            return false;
+        }
+        if (mbar_try(bar, parity)) return true;
+    }
+}
+
+// The loads from tensor memory issued so far are complete; x may be read from here on
+// (as an operand of the wait, so that no use can be scheduled before it).
+__device__ __forceinline__ void wait_loads(float (&x)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]),
+                   "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15])
+                 :
+                 : "memory");
+    asm volatile(""
+                 : "+f"(x[16]), "+f"(x[17]), "+f"(x[18]), "+f"(x[19]), "+f"(x[20]), "+f"(x[21]), "+f"(x[22]),
+                   "+f"(x[23]), "+f"(x[24]), "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]), "+f"(x[29]),
+                   "+f"(x[30]), "+f"(x[31])
+                 :
+                 : "memory");
+}
+
+// One lane of a converged warp, always the same.  The compiler knows that a branch on
+// it holds a single thread and keeps the operands of tcgen05.mma in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Descriptor of a 128-byte-swizzled tile at shared address `s` (smem_desc_sw128 with the
+// strides of these kernels' tiles: 16 KB between 64-column halves, 1 KB between 8-row
+// groups), split so that a step along the tile is one 32-bit addition.
+struct Desc {
+    uint32_t lo;
+    __device__ __forceinline__ explicit Desc(uint32_t s) : lo(((s >> 4) & 0x3FFF) | (16384u >> 4) << 16) {}
+    __device__ __forceinline__ uint64_t at(uint32_t bytes) const {
+        constexpr uint32_t hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+        return (uint64_t)hi << 32 | (lo + (bytes >> 4));
+    }
+};
+
+// D[128 x 128] = A B^T over d (16 d-columns per step), A and B K-major tiles
+template <int D> __device__ __forceinline__ void mma_dots(uint32_t dst, uint32_t a, uint32_t b) {
+    constexpr uint32_t id = idesc_bf16_f32(128, 128, false, false);
+    const Desc da(a), db(b);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+        mma_bf16_ss(dst, da.at((ks >> 2) * 16384 + (ks & 3) * 32), db.at((ks >> 2) * 16384 + (ks & 3) * 32), id, ks > 0);
+}
+// D[128 x d] (+)= A B over 128: A in tensor memory as bf16 pairs, the second 64 of the
+// contracted indices HALF columns behind the first; B a tile whose rows are contracted.
+// Steps [K0, K1) of 16 indices.
+template <int D, int HALF, int K0 = 0, int K1 = 8>
+__device__ __forceinline__ void mma_sum(uint32_t dst, uint32_t a, uint32_t b, uint32_t add) {
+    constexpr uint32_t id = idesc_bf16_f32(128, D, false, true);
+    const Desc db(b);
+#pragma unroll
+    for (int ks = K0; ks < K1; ++ks)
+        mma_bf16_ts(dst, a + (ks >> 2) * HALF + (ks & 3) * 8, db.at(ks * 2048), id, ks > K0 ? 1 : add);
+}
+
+// A position in a ring of N stages: the stage and the parity of its current use.
+template <int N> struct Ring {
+    uint32_t st = 0, ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++st == N) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+// Rows of a ring's tile that are summed over but belong to something else are set to
+// zero by a warp of its own, at the request of the (single) MMA thread, which has seen
+// the tile arrive and waits for `clean` before the product that reads it.  job: the
+// stage (-1: no more requests) and the first row; one request at a time.
+__device__ __forceinline__ void request_clear(uint64_t *req, volatile int *job, int stage, int row) {
+    job[0] = stage;
+    job[1] = row;
+    mbar_arrive(req);
+}
+__device__ __forceinline__ void clear_role(uint8_t *ring, int tile_bytes, int halves, uint64_t *req, uint64_t *clean,
+                                           volatile int *job, volatile int *abort, int lane) {
+    const uint64_t t0 = globaltimer();
+    for (int n = 0;; ++n) {
+        // requests may be far apart: bounded by the life of the kernel (the MMA thread's waits
+        // are bounded, and it ends with a request or with the abort flag set), and by a minute
+        while (!__all_sync(0xffffffffu, mbar_try(req, n & 1)))
+            if (__any_sync(0xffffffffu, *abort != 0 || globaltimer() - t0 > 60000000000ull)) return;
+        const int stage = job[0], row = job[1];
+        if (stage < 0) return;
+        uint8_t *tile = ring + stage * tile_bytes;
+        for (int i = row * 8 + lane; i < 128 * 8; i += 32)
+            for (int h = 0; h < halves; ++h)
+                *reinterpret_cast<uint4 *>(tile + h * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        mbar_arrive_lane0(clean, lane);
+    }
+}
+
 template <int N> __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }

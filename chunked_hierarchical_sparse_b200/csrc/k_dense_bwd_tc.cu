@@ -52,23 +52,6 @@ template <int NH> __device__ __forceinline__ void clear_rows(uint8_t *tile, int 
         for (int h = 0; h < NH; ++h) *reinterpret_cast<uint4 *>(tile + h * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// D[128 x 128] = A B^T over d, both tiles K-major in shared memory
-template <int D> __device__ __forceinline__ void mma_dots(uint32_t dst, uint32_t a, uint32_t b) {
-    constexpr uint32_t id = idesc_bf16_f32(128, kTile, false, false);
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-        mma_bf16_ss(dst, smem_desc_sw128(a + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                    smem_desc_sw128(b + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), id, ks > 0);
-}
-// D[128 x d] (+)= A B, A in tensor memory (the two warpgroups' halves, 64 of the 128
-// contracted indices each, 64 columns apart), B a tile with the contracted index as its rows
-template <int D> __device__ __forceinline__ void mma_sum(uint32_t dst, uint32_t a, uint32_t b, bool add) {
-    constexpr uint32_t id = idesc_bf16_f32(128, D, false, true);
-#pragma unroll
-    for (int ks = 0; ks < kTile / 16; ++ks)
-        mma_bf16_ts(dst, a + (ks >> 2) * 64 + (ks & 3) * 8, smem_desc_sw128(b + ks * 2048, 16384, 1024), id, add || ks > 0);
-}
-
 __device__ __forceinline__ void load64(uint32_t t, float (&x)[64]) {
     float(&x0)[32] = *reinterpret_cast<float(*)[32]>(x);
     float(&x1)[32] = *reinterpret_cast<float(*)[32]>(x + 32);
@@ -130,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int tt = 128 / a.G, rows = tt * a.G;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -160,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + D;
     auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
     // row tiles of an item: from the one that holds its first key's token to the sequence's end
@@ -236,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             if (t.end) break;
             if (!(ok = wait(fix_full, n, 12))) break;
             const uint32_t kb = smem_u32(sm + L::OFF_FIX), vb = kb + L::TILE;
-            const int j0 = first_tile(t), j1 = end_tile(t);
+            const int j0 = uniform(first_tile(t)), j1 = uniform(end_tile(t));
             auto ring = [&](int p) { return smem_u32(sm + L::OFF_RING + (p % L::ST) * L::TILE); };
             // tile j's Q (o = 0) or dO (o = 1) is in shared memory; rows behind the sequence's last
             // token are another's (or nothing's): cleared, since the sums run over all 128 rows
@@ -251,38 +234,38 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                 return true;
             };
             if (!(ok = ready(pos, j0))) break;
-            if (lane == 0) { tc_fence_after(); mma_dots<D>(t_s, kb, ring(pos)); mma_commit(s_full); }
+            if (elect_one()) { tc_fence_after(); mma_dots<D>(t_s, kb, ring(pos)); mma_commit(s_full); }
             if (!(ok = ready(pos + 1, j0))) break;
-            if (lane == 0) { mma_dots<D>(t_dp, vb, ring(pos + 1)); mma_commit(dp_full); }
+            if (elect_one()) { mma_dots<D>(t_dp, vb, ring(pos + 1)); mma_commit(dp_full); }
             for (int j = j0; j < j1; ++j) {
                 const int pq = pos, pd = pos + 1;
                 const bool more = j + 1 < j1;
                 if (!(ok = wait(p_full, np, 12))) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     tc_fence_after();
-                    mma_sum<D>(t_dv, t_s, ring(pd), j > j0);
+                    mma_sum<D, 64>(t_dv, t_s, ring(pd), j > j0);
                     mma_commit(&ring_empty[pd % L::ST]);
                 }
                 if (more) {
                     if (!(ok = ready(pos + 2, j + 1))) break;
-                    if (lane == 0) { tc_fence_after(); mma_dots<D>(t_s, kb, ring(pos + 2)); mma_commit(s_full); }
+                    if (elect_one()) { tc_fence_after(); mma_dots<D>(t_s, kb, ring(pos + 2)); mma_commit(s_full); }
                 }
                 if (!(ok = wait(ds_full, np, 12))) break;
                 ++np;
-                if (lane == 0) {
+                if (elect_one()) {
                     tc_fence_after();
-                    mma_sum<D>(t_dk, t_dp, ring(pq), j > j0);
+                    mma_sum<D, 64>(t_dk, t_dp, ring(pq), j > j0);
                     mma_commit(&ring_empty[pq % L::ST]);
                     if (!more) { mma_commit(acc_full); mma_commit(fix_empty); }
                 }
                 if (more) {
                     if (!(ok = ready(pos + 3, j + 1))) break;
-                    if (lane == 0) { tc_fence_after(); mma_dots<D>(t_dp, vb, ring(pos + 3)); mma_commit(dp_full); }
+                    if (elect_one()) { tc_fence_after(); mma_dots<D>(t_dp, vb, ring(pos + 3)); mma_commit(dp_full); }
                 }
                 pos += 2;
             }
         }
-        if (!ok && lane == 0) {  // the MMAs issued so far end before tensor memory is freed (bounded)
+        if (!ok && elect_one()) {  // the MMAs issued so far end before tensor memory is freed (bounded)
             mma_commit(done);
             mbar_wait(done, 0, kDrainWaitNs);
         }
@@ -410,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int tt = 128 / a.G, rows = tt * a.G;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 9); mbar_init(&s_full[i], 1); }
@@ -431,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;  // S: two buffers
     auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
     auto tiles = [](int keys) { return (keys + kTile - 1) / kTile; };
@@ -505,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
             if (t.end) break;
             if (!(ok = wait(fix_full, n, 22))) break;
             const uint32_t qb = smem_u32(sm + L::OFF_FIX), ob = qb + L::TILE;
-            const int nn = tiles(t.nkeys);
+            const int nn = uniform(tiles(t.nkeys));
             auto ring = [&](int p) { return smem_u32(sm + L::OFF_RING + (p % L::ST) * L::TILE); };
             auto scores = [&](int j) -> bool {  // S of key tile j, into buffer nt & 1 of that tile
                 const int p = pos + 2 * j;
@@ -515,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if (lane == 0) {
+                if (elect_one()) {
                     tc_fence_after();
                     const int sb = (nt + j) & 1;
                     mma_dots<D>(t_s + sb * 128, qb, ring(p));
@@ -526,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
             auto dprob = [&](int j) -> bool {
                 const int p = pos + 2 * j + 1;
                 if (!wait(&ring_full[p % L::ST], p / L::ST, 22)) return false;
-                if (lane == 0) {
+                if (elect_one()) {
                     tc_fence_after();
                     mma_dots<D>(t_dp, ob, ring(p));
                     mma_commit(dp_full);
@@ -545,10 +528,10 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                     break;
                 }
                 if (!(ok = wait(ds_full, nt + j, 22))) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     tc_fence_after();
                     const int p = pos + 2 * j;
-                    mma_sum<D>(t_dq, t_s + ((nt + j) & 1) * 128, ring(p), j > 0);
+                    mma_sum<D, 64>(t_dq, t_s + ((nt + j) & 1) * 128, ring(p), j > 0);
                     mma_commit(&ring_empty[p % L::ST]);
                     if (j == nn - 1) mma_commit(acc_full);
                 }
@@ -556,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
             pos += 2 * nn;
             nt += nn;
         }
-        if (!ok && lane == 0) {
+        if (!ok && elect_one()) {
             mma_commit(done);
             mbar_wait(done, 0, kDrainWaitNs);
         }

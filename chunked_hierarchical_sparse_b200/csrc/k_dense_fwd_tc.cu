@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kKeys = 128;        // keys per tile
-constexpr int kWarpLoad = 8, kWarpMma = 9;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpClear = 10;
 constexpr int kItems = 2;         // item ring
 constexpr float kSlack = 8.f;     // log2 of how far a tile may exceed m before it moves
 
@@ -86,6 +86,25 @@ __device__ __forceinline__ bool get_tc_item(const Args &a, int i, TcItem &t) {
     return some;
 }
 
+// this warp's lanes, 16 columns of an accumulator, times f (few registers: the caller holds a row of S)
+__device__ __forceinline__ void rescale16(uint32_t t, float f) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
@@ -100,19 +119,20 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
     uint64_t *item_full = bar, *item_empty = bar + kItems;
     uint64_t *q_full = item_empty + kItems, *q_empty = q_full + 2;
     uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2;
-    uint64_t *done = o_full + 2;
+    uint64_t *p_half = o_full + 2, *clean = p_half + 2, *clear_req = clean + 1, *done = clear_req + 1;
     uint64_t *kv_full = done + 1, *kv_empty = kv_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
+    volatile int *clear_job = abort_flag + 1;  // stage, first row
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kItems; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 9); }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
-            mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1);
+            mbar_init(&s_full[i], 1); mbar_init(&p_half[i], 4); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1);
         }
-        mbar_init(done, 1);
+        mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1); }
         *abort_flag = 0;
         mbar_fence_init();
@@ -127,12 +147,12 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     auto wait = [&](uint64_t *b, uint32_t par, int role) { return warp_wait(b, par & 1, wait_ns, abort_flag, a.ds, role); };
     auto tiles = [](int keys) { return (keys + kKeys - 1) / kKeys; };
 
     if (warp >= 8) {
-        reg_dec<56>();
+        reg_dec<72>();
         if (warp == kWarpLoad) {
             // ======================================================== items and loads
             const int total = item_count(a);
@@ -211,101 +231,101 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             }
             __syncwarp();
         } else if (warp == kWarpMma) {
-            // ======================================================== MMA issue
-            constexpr uint32_t id_s = idesc_bf16_f32(128, kKeys, false, false);
-            constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
-            int kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-            bool ok = true;
-            for (int n = 0; ok; ++n) {
-                const int ib = n % kItems;
-                if (!(ok = wait(&item_full[ib], n / kItems, 2))) break;
-                const TcItem t = items[ib];
-                __syncwarp();
-                mbar_arrive_lane0(&item_empty[ib], lane);
-                if (t.end) break;
-                const int n0 = tiles(t.nkeys[0]), n1 = tiles(t.nkeys[1]), nn = max(n0, n1);
-                // ring positions: shared -- K(j) = base + 2 j, V(j) = base + 2 j + 1; else in order of use
-                const int base = kv;
-                int k_at[2], v_at = 0;  // position of the K tile that S(s) uses next
-                if (t.shared) {
-                    k_at[0] = k_at[1] = base;
-                } else {
-                    k_at[0] = base;
-                    k_at[1] = base + 1;
-                    kv = base + (n1 ? 2 : 1);
-                }
-                auto scores = [&](int s, int j, int ns) -> bool {  // S(s) of tile j
-                    const int st = k_at[s] % L::ST;
-                    if (j == 0 && !wait(&q_full[s], nq[s], 2)) return false;
-                    if (!wait(&kv_full[st], k_at[s] / L::ST, 2)) return false;
-                    if (lane == 0) {
-                        tc_fence_after();
-                        const uint32_t qa = smem_u32(sm + L::OFF_Q + s * L::TILE);
-                        const uint32_t kb = smem_u32(sm + L::OFF_KV + st * L::TILE);
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            mma_bf16_ss(tmem + s * 128, smem_desc_sw128(qa + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                                        smem_desc_sw128(kb + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), id_s, ks > 0);
-                        mma_commit(&s_full[s]);
-                        if (j == ns - 1) mma_commit(&q_empty[s]);
-                        // the K tile is free once the last stream that reads it has
-                        if (!t.shared || s == 1 || j >= n1) mma_commit(&kv_empty[st]);
-                    }
-                    if (j == ns - 1) ++nq[s];
-                    return true;
-                };
-                ok = scores(0, 0, n0);
-                if (ok && n1) ok = scores(1, 0, n1);
-                for (int j = 0; ok && j < nn; ++j) {
+            // ======================================================== MMA issue, a single thread
+            // One thread issues for both streams, in turns: the products then run first come, first
+            // served, one stream's while the other's softmax works.  (Two issuing warps interleave
+            // the streams' products, both finish late and both softmaxes run at the same time:
+            // 1185 instead of MEASURED TFLOP/s at 64K tokens.)
+            if (elect_one()) {
+                auto wait1 = [&](uint64_t *b, uint32_t par) { return thread_wait(b, par & 1, wait_ns, abort_flag, a.ds, 2); };
+                Ring<L::ST> kv;
+                int nq[2] = {0, 0}, np[2] = {0, 0}, nc = 0;
+                bool ok = true;
+                for (int n = 0; ok; ++n) {
+                    const int ib = n % kItems;
+                    if (!(ok = wait1(&item_full[ib], n / kItems))) break;
+                    const TcItem t = items[ib];
+                    mbar_arrive(&item_empty[ib]);
+                    if (t.end) break;
+                    const bool shared = t.shared;
+                    const int n0 = tiles(t.nkeys[0]), n1 = tiles(t.nkeys[1]), nn = max(n0, n1);
+                    // Tiles in the order of the loads: shared, K(j) V(j) for both streams; else K0(0) [K1(0)],
+                    // then per j V0(j) K0(j+1) V1(j) K1(j+1), as far as each stream goes.
+                    // A shared tile is free once the last stream that reads it has.
+                    auto last_reader = [&](int s, int j) { return !shared || s == 1 || j >= n1; };
+                    Ring<L::ST> v, k;  // the tiles in hand
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const int ns = s ? n1 : n0;
-                        if (!ok || j >= ns) continue;
-                        v_at = t.shared ? base + 2 * j + 1 : kv++;
-                        const int st = v_at % L::ST;
-                        if (!(ok = wait(&kv_full[st], v_at / L::ST, 2))) break;
-                        // values behind the last key belong to something else and may be anything:
-                        // their weights are 0, and 0 * NaN is NaN, so they are cleared
-                        if (t.foreign && (t.shared ? j == nn - 1 && s == (n0 != nn) : j == ns - 1)) {
-                            const int last = t.shared ? max(t.nkeys[0], t.nkeys[1]) : t.nkeys[s];
-                            const int r0 = last - j * kKeys;
-                            uint8_t *vb = sm + L::OFF_KV + st * L::TILE;
-                            for (int i = r0 * 8 + lane; i < kKeys * 8; i += 32)
-#pragma unroll
-                                for (int h = 0; h < L::NH; ++h)
-                                    *reinterpret_cast<uint4 *>(vb + h * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
-                            fence_proxy_async_smem();
-                            __syncwarp();
+                        if (!ok || (s ? n1 : n0) == 0) continue;
+                        if (s == 0 || !shared) {
+                            k = kv;
+                            kv.next();
+                            if (!(ok = wait1(&kv_full[k.st], k.ph))) break;
                         }
-                        if (!(ok = wait(&p_full[s], np[s], 2))) break;
-                        ++np[s];
-                        if (lane == 0) {
+                        if (!(ok = wait1(&q_full[s], nq[s]++))) break;
+                        tc_fence_after();
+                        mma_dots<D>(tmem + s * 128, smem_u32(sm + L::OFF_Q + s * L::TILE), smem_u32(sm + L::OFF_KV + k.st * L::TILE));
+                        mma_commit(&s_full[s]);
+                        if (last_reader(s, 0)) mma_commit(&kv_empty[k.st]);
+                        if ((s ? n1 : n0) == 1) mma_commit(&q_empty[s]);
+                    }
+                    for (int j = 0; ok && j < nn; ++j) {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const int ns = s ? n1 : n0;
+                            if (!ok || j >= ns) continue;
+                            const bool more = j + 1 < ns;
+                            if (!shared || s == 0 || j >= n0) {  // V(j) and K(j+1): the next two tiles
+                                v = kv;
+                                kv.next();
+                                if (!(ok = wait1(&kv_full[v.st], v.ph))) break;
+                                if (shared ? j + 1 < nn : more) {
+                                    k = kv;
+                                    kv.next();
+                                    if (!(ok = wait1(&kv_full[k.st], k.ph))) break;
+                                }
+                            }
+                            // values behind the last key belong to something else and may be anything:
+                            // their weights are 0, and 0 * NaN is NaN, so warp 10 clears them meanwhile
+                            const int last = shared ? max(t.nkeys[0], t.nkeys[1]) : t.nkeys[s];
+                            const bool dirty = t.foreign && last % kKeys != 0 && j == (shared ? nn : ns) - 1 &&
+                                               (!shared || s == (n0 != nn));
+                            if (dirty) request_clear(clear_req, clear_job, v.st, last % kKeys);
+                            const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * D;
+                            const uint32_t vs = smem_u32(sm + L::OFF_KV + v.st * L::TILE);
+                            // the first half of P is multiplied while the second is still exponentials
+                            if (!(ok = (!dirty || wait1(clean, nc++)) && wait1(&p_half[s], np[s]))) break;
                             tc_fence_after();
-                            const uint32_t vb = smem_u32(sm + L::OFF_KV + st * L::TILE);
-#pragma unroll
-                            for (int ks = 0; ks < kKeys / 16; ++ks)
-                                mma_bf16_ts(tmem + 256 + s * D, tmem + s * 128 + ks * 8,
-                                            smem_desc_sw128(vb + ks * 2048, 16384, 1024), id_o, j > 0 || ks > 0);
-                            if (!t.shared || s == 1 || j >= n1) mma_commit(&kv_empty[st]);
-                            if (j == ns - 1) mma_commit(&o_full[s]);
-                        }
-                        if (j + 1 < ns) {
-                            k_at[s] = t.shared ? base + 2 * (j + 1) : kv++;
-                            ok = scores(s, j + 1, ns);
+                            mma_sum<D, 32, 0, 4>(t_o, t_s, vs, j > 0);
+                            if (!(ok = wait1(&p_full[s], np[s]++))) break;
+                            tc_fence_after();
+                            mma_sum<D, 32, 4, 8>(t_o, t_s, vs, 1);
+                            if (more) {
+                                mma_dots<D>(t_s, smem_u32(sm + L::OFF_Q + s * L::TILE), smem_u32(sm + L::OFF_KV + k.st * L::TILE));
+                                mma_commit(&s_full[s]);
+                                if (last_reader(s, j + 1)) mma_commit(&kv_empty[k.st]);
+                                if (j + 2 == ns) mma_commit(&q_empty[s]);
+                            } else {
+                                mma_commit(&o_full[s]);
+                            }
+                            if (last_reader(s, j)) mma_commit(&kv_empty[v.st]);
                         }
                     }
                 }
-                if (t.shared) kv = base + 2 * nn;
-            }
-            if (!ok && lane == 0) {  // the MMAs issued so far end before tensor memory is freed (bounded)
-                mma_commit(done);
-                mbar_wait(done, 0, kDrainWaitNs);
+                request_clear(clear_req, clear_job, -1, 0);
+                if (!ok) {  // the MMAs issued so far end before tensor memory is freed (bounded)
+                    mma_commit(done);
+                    mbar_wait(done, 0, kDrainWaitNs);
+                }
             }
             __syncwarp();
+        } else if (warp == kWarpClear) {
+            // ======================================================== values behind the last key
+            clear_role(sm + L::OFF_KV, L::TILE, L::NH, clear_req, clean, clear_job, abort_flag, lane);
         }
     } else {
         // ============================================================ softmax, one warpgroup per stream
-        reg_inc<224>();
+        reg_inc<216>();
         const int s = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256 + s * D;
@@ -333,58 +353,57 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                 if (warp_rows) {
                     tc_fence_after();
                     float x[128];
-                    {
-                        float(&x0)[32] = *reinterpret_cast<float(*)[32]>(x);
-                        float(&x1)[32] = *reinterpret_cast<float(*)[32]>(x + 32);
-                        float(&x2)[32] = *reinterpret_cast<float(*)[32]>(x + 64);
-                        float(&x3)[32] = *reinterpret_cast<float(*)[32]>(x + 96);
-                        tmem_ld32(ts, x0);
-                        tmem_ld32(ts + 32, x1);
-                        tmem_ld32(ts + 64, x2);
-                        tmem_ld32(ts + 96, x3);
-                        tmem_wait_ld();
-                    }
-                    if (j * kKeys + kKeys - 1 > lim_all) {
-                        const int last = lim - j * kKeys;
+                    float(&x0)[32] = *reinterpret_cast<float(*)[32]>(x);
+                    float(&x1)[32] = *reinterpret_cast<float(*)[32]>(x + 32);
+                    float(&x2)[32] = *reinterpret_cast<float(*)[32]>(x + 64);
+                    float(&x3)[32] = *reinterpret_cast<float(*)[32]>(x + 96);
+                    tmem_ld32(ts, x0);
+                    tmem_ld32(ts + 32, x1);
+                    wait_loads(x0);
+                    wait_loads(x1);
+                    tmem_ld32(ts + 64, x2);  // in flight while the first half is worked on
+                    tmem_ld32(ts + 96, x3);
+                    const bool edge = j * kKeys + kKeys - 1 > lim_all;
+                    const int last = lim - j * kKeys;
+                    if (edge) {
 #pragma unroll
-                        for (int i = 0; i < 128; ++i) x[i] = i <= last ? x[i] : -INFINITY;
+                        for (int i = 0; i < 64; ++i) x[i] = i <= last ? x[i] : -INFINITY;
                     }
-                    float mx0 = x[0], mx1 = x[1];
+                    if (j == 0 || edge) {
+                        wait_loads(x2);
+                        wait_loads(x3);
+                    }
+                    if (edge) {
 #pragma unroll
-                    for (int i = 2; i < 128; i += 4) {
-                        mx0 = fmaxf(mx0, fmaxf(x[i], i + 2 < 128 ? x[i + 2] : x[i]));
-                        mx1 = fmaxf(mx1, fmaxf(x[i + 1], i + 3 < 128 ? x[i + 3] : x[i + 1]));
+                        for (int i = 64; i < 128; ++i) x[i] = i <= last ? x[i] : -INFINITY;
                     }
-                    const float mx = fmaxf(mx0, mx1) * c;
                     if (j == 0) {
-                        m = mx;
-                    } else if (__any_sync(0xffffffffu, mx > m + kSlack)) {
-                        const float f = mx > m + kSlack ? ex2(m - mx) : 1.f;
-                        m = mx > m + kSlack ? mx : m;
-                        l *= f;
-                        // S(j) is complete, so P.V(j-1) issued before it is, too
+                        float mxs[8];
 #pragma unroll
-                        for (int h = 0; h < D / 32; ++h) {
-                            float y[32];
-                            uint32_t u[32];
-                            tmem_ld32(to + h * 32, y);
-                            tmem_wait_ld();
+                        for (int i = 0; i < 8; ++i) mxs[i] = fmaxf(x[i], x[i + 8]);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(y[i] * f);
-                            tmem_st32(to + h * 32, u);
-                        }
+                        for (int i = 16; i < 128; i += 16)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) mxs[e] = fmaxf(fmaxf(mxs[e], x[i + e]), x[i + 8 + e]);
+                        m = c * fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
+                                      fmaxf(fmaxf(mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7])));
                     }
-                    const float mn = m == -INFINITY ? 0.f : -m;
-                    const float2 c2 = make_float2(c, c), m2 = make_float2(mn, mn);
-                    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t u[32];
+                    // Later tiles take their exponentials from the m so far; the tile's maximum is
+                    // found meanwhile (other pipe), and if it exceeds m by too much, once more.
+                    const float2 c2 = make_float2(c, c);
+                    float2 sum0, sum1;
+                    uint32_t u[32];
+                    while (true) {
+                        const float mn = m == -INFINITY ? 0.f : -m;
+                        const float2 m2 = make_float2(mn, mn);
+                        float mx0 = x[0], mx1 = x[1];
+                        sum0 = sum1 = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            const int e = h * 64 + 2 * i;
-                            float2 y0 = fma2(make_float2(x[e], x[e + 1]), c2, m2);
-                            float2 y1 = fma2(make_float2(x[e + 2], x[e + 3]), c2, m2);
+                            float2 y0 = fma2(make_float2(x[2 * i], x[2 * i + 1]), c2, m2);
+                            float2 y1 = fma2(make_float2(x[2 * i + 2], x[2 * i + 3]), c2, m2);
+                            mx0 = fmaxf(fmaxf(mx0, x[2 * i]), x[2 * i + 1]);
+                            mx1 = fmaxf(fmaxf(mx1, x[2 * i + 2]), x[2 * i + 3]);
                             y0.x = ex2(y0.x); y0.y = ex2(y0.y);
                             y1.x = ex2(y1.x); y1.y = ex2(y1.y);
                             sum0 = add2(sum0, y0);
@@ -392,15 +411,58 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                             u[i] = bf16_pair(y0.x, y0.y);
                             u[i + 1] = bf16_pair(y1.x, y1.y);
                         }
-                        tmem_st32(ts + h * 32, u);
+                        wait_loads(x2);
+                        wait_loads(x3);
+                        float mx2 = x[64], mx3 = x[65];
+#pragma unroll
+                        for (int i = 66; i < 126; i += 4) {
+                            mx0 = fmaxf(fmaxf(mx0, x[i]), x[i + 1]);
+                            mx1 = fmaxf(fmaxf(mx1, x[i + 2]), x[i + 3]);
+                        }
+                        mx2 = fmaxf(mx2, x[126]);
+                        mx3 = fmaxf(mx3, x[127]);
+                        const float mx = c * fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+                        if (!__any_sync(0xffffffffu, mx > m + kSlack)) break;
+                        const float f = mx > m + kSlack ? ex2(m - mx) : 1.f;
+                        m = mx > m + kSlack ? mx : m;
+                        l *= f;
+                        if (j == 0) continue;
+                        // S(j) is complete, so P.V(j-1) issued before it is, too
+#pragma unroll
+                        for (int h = 0; h < D / 16; ++h) rescale16(to + h * 16, f);
+                        tmem_wait_st();
                     }
-                    sum0 = add2(sum0, sum1);
-                    l += sum0.x + sum0.y;
+                    tmem_st32(ts, u);
                     tmem_wait_st();
                     tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_lane0(&p_half[s], lane);
+                    {
+                        const float mn = m == -INFINITY ? 0.f : -m;
+                        const float2 m2 = make_float2(mn, mn);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float2 y0 = fma2(make_float2(x[2 * i + 64], x[2 * i + 65]), c2, m2);
+                            float2 y1 = fma2(make_float2(x[2 * i + 66], x[2 * i + 67]), c2, m2);
+                            y0.x = ex2(y0.x); y0.y = ex2(y0.y);
+                            y1.x = ex2(y1.x); y1.y = ex2(y1.y);
+                            sum0 = add2(sum0, y0);
+                            sum1 = add2(sum1, y1);
+                            u[i] = bf16_pair(y0.x, y0.y);
+                            u[i + 1] = bf16_pair(y1.x, y1.y);
+                        }
+                    }
+                    tmem_st32(ts + 32, u);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_lane0(&p_full[s], lane);
+                    sum0 = add2(sum0, sum1);
+                    l += sum0.x + sum0.y;
+                } else {
+                    mbar_arrive_lane0(&p_half[s], lane);
+                    mbar_arrive_lane0(&p_full[s], lane);
                 }
-                __syncwarp();
-                mbar_arrive_lane0(&p_full[s], lane);
             }
             if (!ok || !(ok = wait(&o_full[s], no_done, 3))) break;
             ++no_done;
