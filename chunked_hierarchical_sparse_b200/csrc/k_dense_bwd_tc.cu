@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kTile = 128;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpStat = 10;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpStat = 10, kWarpClear = 11;
 constexpr int kItems = 2;
 
 template <int D, bool KEYS> struct Smem {
@@ -45,19 +45,13 @@ template <int D, bool KEYS> struct Smem {
 };
 static_assert(Smem<128, true>::ALLOC <= 232448 && Smem<128, false>::ALLOC <= 232448, "shared memory of a CTA");
 
-// rows [r0, 128) of a swizzled tile set to zero by one warp, before MMAs read it
-template <int NH> __device__ __forceinline__ void clear_rows(uint8_t *tile, int r0, int lane) {
-    for (int i = r0 * 8 + lane; i < kTile * 8; i += 32)
-#pragma unroll
-        for (int h = 0; h < NH; ++h) *reinterpret_cast<uint4 *>(tile + h * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
-}
-
 __device__ __forceinline__ void load64(uint32_t t, float (&x)[64]) {
     float(&x0)[32] = *reinterpret_cast<float(*)[32]>(x);
     float(&x1)[32] = *reinterpret_cast<float(*)[32]>(x + 32);
     tmem_ld32(t, x0);
     tmem_ld32(t + 32, x1);
-    tmem_wait_ld();
+    wait_loads(x0);
+    wait_loads(x1);
 }
 __device__ __forceinline__ void store64(uint32_t t, const float (&x)[64]) {  // as 32 bf16 pairs
     uint32_t u[32];
@@ -109,9 +103,10 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     uint64_t *item_full = bar, *item_empty = bar + 2, *fix_full = bar + 4, *fix_empty = bar + 5;
     uint64_t *stat_full = bar + 6, *stat_empty = bar + 8;
     uint64_t *s_full = bar + 10, *dp_full = bar + 11, *p_full = bar + 12, *ds_full = bar + 13, *acc_full = bar + 14;
-    uint64_t *done = bar + 15, *ring_full = bar + 16, *ring_empty = ring_full + L::ST;
+    uint64_t *done = bar + 15, *clean = bar + 16, *clear_req = bar + 17, *ring_full = bar + 18, *ring_empty = ring_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
+    volatile int *clear_job = abort_flag + 1;  // stage, first row
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int tt = 128 / a.G, rows = tt * a.G;
@@ -122,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
         }
         mbar_init(fix_full, 1); mbar_init(fix_empty, 1);
         mbar_init(s_full, 1); mbar_init(dp_full, 1); mbar_init(p_full, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
-        mbar_init(done, 1);
+        mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
         *abort_flag = 0;
         mbar_fence_init();
@@ -207,69 +202,75 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
-        // ============================================================ MMA issue
-        int pos = 0, np = 0;
-        bool ok = true;
-        for (int n = 0; ok; ++n) {
-            const int ib = n % kItems;
-            if (!(ok = wait(&item_full[ib], n / kItems, 12))) break;
-            const BwdItem t = items[ib];
-            __syncwarp();
-            mbar_arrive_lane0(&item_empty[ib], lane);
-            if (t.end) break;
-            if (!(ok = wait(fix_full, n, 12))) break;
+        // ============================================================ MMA issue, a single thread
+        if (elect_one()) {
+            auto wait1 = [&](uint64_t *x, uint32_t par) { return thread_wait(x, par & 1, wait_ns, abort_flag, a.ds, 12); };
             const uint32_t kb = smem_u32(sm + L::OFF_FIX), vb = kb + L::TILE;
-            const int j0 = uniform(first_tile(t)), j1 = uniform(end_tile(t));
-            auto ring = [&](int p) { return smem_u32(sm + L::OFF_RING + (p % L::ST) * L::TILE); };
-            // tile j's Q (o = 0) or dO (o = 1) is in shared memory; rows behind the sequence's last
-            // token are another's (or nothing's): cleared, since the sums run over all 128 rows
-            auto ready = [&](int p, int j) -> bool {
-                if (!wait(&ring_full[p % L::ST], p / L::ST, 12)) return false;
-                const int real = (t.ntok - j * tt) * a.G;
-                if (real < rows) {
-                    clear_rows<L::NH>(sm + L::OFF_RING + (p % L::ST) * L::TILE, real, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                return true;
-            };
-            if (!(ok = ready(pos, j0))) break;
-            if (elect_one()) { tc_fence_after(); mma_dots<D>(t_s, kb, ring(pos)); mma_commit(s_full); }
-            if (!(ok = ready(pos + 1, j0))) break;
-            if (elect_one()) { mma_dots<D>(t_dp, vb, ring(pos + 1)); mma_commit(dp_full); }
-            for (int j = j0; j < j1; ++j) {
-                const int pq = pos, pd = pos + 1;
-                const bool more = j + 1 < j1;
-                if (!(ok = wait(p_full, np, 12))) break;
-                if (elect_one()) {
+            Ring<L::ST> ring;
+            int np = 0, nc = 0;
+            bool ok = true;
+            for (int n = 0; ok; ++n) {
+                const int ib = n % kItems;
+                if (!(ok = wait1(&item_full[ib], n / kItems))) break;
+                const BwdItem t = items[ib];
+                mbar_arrive(&item_empty[ib]);
+                if (t.end) break;
+                const int j0 = first_tile(t), j1 = end_tile(t);
+                auto tile = [&](const Ring<L::ST> &r) { return smem_u32(sm + L::OFF_RING + r.st * L::TILE); };
+                // Tile j's Q or dO, as loaded next.  Rows behind the sequence's last token are
+                // another's (or nothing's): cleared, since the sums run over all 128 rows.
+                auto take = [&](int j, Ring<L::ST> &r) -> bool {
+                    r = ring;
+                    ring.next();
+                    if (!wait1(&ring_full[r.st], r.ph)) return false;
+                    const int real = (t.ntok - j * tt) * a.G;
+                    if (real >= rows) return true;
+                    request_clear(clear_req, clear_job, r.st, real);
+                    return wait1(clean, nc++);
+                };
+                Ring<L::ST> q, d, qn;
+                if (!(ok = wait1(fix_full, n) && take(j0, q))) break;
+                tc_fence_after();
+                mma_dots<D>(t_s, kb, tile(q));
+                mma_commit(s_full);
+                if (!(ok = take(j0, d))) break;
+                mma_dots<D>(t_dp, vb, tile(d));
+                mma_commit(dp_full);
+                for (int j = j0; j < j1; ++j) {
+                    const bool more = j + 1 < j1;
+                    if (more && !(ok = take(j + 1, qn))) break;
+                    if (!(ok = wait1(p_full, np))) break;
                     tc_fence_after();
-                    mma_sum<D, 64>(t_dv, t_s, ring(pd), j > j0);
-                    mma_commit(&ring_empty[pd % L::ST]);
-                }
-                if (more) {
-                    if (!(ok = ready(pos + 2, j + 1))) break;
-                    if (elect_one()) { tc_fence_after(); mma_dots<D>(t_s, kb, ring(pos + 2)); mma_commit(s_full); }
-                }
-                if (!(ok = wait(ds_full, np, 12))) break;
-                ++np;
-                if (elect_one()) {
+                    mma_sum<D, 64>(t_dv, t_s, tile(d), j > j0);
+                    if (more) {
+                        mma_dots<D>(t_s, kb, tile(qn));
+                        mma_commit(s_full);
+                    }
+                    mma_commit(&ring_empty[d.st]);
+                    if (more && !(ok = take(j + 1, d))) break;
+                    if (!(ok = wait1(ds_full, np++))) break;
                     tc_fence_after();
-                    mma_sum<D, 64>(t_dk, t_dp, ring(pq), j > j0);
-                    mma_commit(&ring_empty[pq % L::ST]);
-                    if (!more) { mma_commit(acc_full); mma_commit(fix_empty); }
+                    mma_sum<D, 64>(t_dk, t_dp, tile(q), j > j0);
+                    if (more) {
+                        mma_dots<D>(t_dp, vb, tile(d));
+                        mma_commit(dp_full);
+                    } else {
+                        mma_commit(acc_full);
+                        mma_commit(fix_empty);
+                    }
+                    mma_commit(&ring_empty[q.st]);
+                    q = qn;
                 }
-                if (more) {
-                    if (!(ok = ready(pos + 3, j + 1))) break;
-                    if (elect_one()) { tc_fence_after(); mma_dots<D>(t_dp, vb, ring(pos + 3)); mma_commit(dp_full); }
-                }
-                pos += 2;
+            }
+            request_clear(clear_req, clear_job, -1, 0);
+            if (!ok) {  // the MMAs issued so far end before tensor memory is freed (bounded)
+                mma_commit(done);
+                mbar_wait(done, 0, kDrainWaitNs);
             }
         }
-        if (!ok && elect_one()) {  // the MMAs issued so far end before tensor memory is freed (bounded)
-            mma_commit(done);
-            mbar_wait(done, 0, kDrainWaitNs);
-        }
         __syncwarp();
+    } else if (warp == kWarpClear) {
+        clear_role(sm + L::OFF_RING, L::TILE, L::NH, clear_req, clean, clear_job, abort_flag, lane);
     } else if (warp == kWarpStat) {
         // ============================================================ row statistics of each tile
         int nt = 0;
@@ -389,9 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
     uint64_t *item_full = bar, *item_empty = bar + 2, *fix_full = bar + 4, *fix_empty = bar + 5;
     uint64_t *s_full = bar + 6, *dp_full = bar + 8, *dp_read = bar + 9, *ds_full = bar + 10, *acc_full = bar + 11;
-    uint64_t *done = bar + 12, *ring_full = bar + 13, *ring_empty = ring_full + L::ST;
+    uint64_t *done = bar + 12, *clean = bar + 13, *clear_req = bar + 14, *ring_full = bar + 15, *ring_empty = ring_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
+    volatile int *clear_job = abort_flag + 1;  // stage, first row
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int tt = 128 / a.G, rows = tt * a.G;
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
         for (int i = 0; i < 2; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 9); mbar_init(&s_full[i], 1); }
         mbar_init(fix_full, 1); mbar_init(fix_empty, 1);
         mbar_init(dp_full, 1); mbar_init(dp_read, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
-        mbar_init(done, 1);
+        mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
         *abort_flag = 0;
         mbar_fence_init();
@@ -476,74 +478,74 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
-        // ============================================================ MMA issue
-        int pos = 0, nt = 0;
-        bool ok = true;
-        for (int n = 0; ok; ++n) {
-            const int ib = n % kItems;
-            if (!(ok = wait(&item_full[ib], n / kItems, 22))) break;
-            const BwdItem t = items[ib];
-            __syncwarp();
-            mbar_arrive_lane0(&item_empty[ib], lane);
-            if (t.end) break;
-            if (!(ok = wait(fix_full, n, 22))) break;
+        // ============================================================ MMA issue, a single thread
+        if (elect_one()) {
+            auto wait1 = [&](uint64_t *x, uint32_t par) { return thread_wait(x, par & 1, wait_ns, abort_flag, a.ds, 22); };
             const uint32_t qb = smem_u32(sm + L::OFF_FIX), ob = qb + L::TILE;
-            const int nn = uniform(tiles(t.nkeys));
-            auto ring = [&](int p) { return smem_u32(sm + L::OFF_RING + (p % L::ST) * L::TILE); };
-            auto scores = [&](int j) -> bool {  // S of key tile j, into buffer nt & 1 of that tile
-                const int p = pos + 2 * j;
-                if (!wait(&ring_full[p % L::ST], p / L::ST, 22)) return false;
-                if (t.foreign && j == nn - 1) {  // dS is 0 there, but 0 * NaN is not
-                    clear_rows<L::NH>(sm + L::OFF_RING + (p % L::ST) * L::TILE, t.nkeys - j * kTile, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (elect_one()) {
-                    tc_fence_after();
+            Ring<L::ST> ring;
+            int nt = 0, nc = 0;
+            bool ok = true;
+            for (int n = 0; ok; ++n) {
+                const int ib = n % kItems;
+                if (!(ok = wait1(&item_full[ib], n / kItems))) break;
+                const BwdItem t = items[ib];
+                mbar_arrive(&item_empty[ib]);
+                if (t.end) break;
+                if (!(ok = wait1(fix_full, n))) break;
+                const int nn = tiles(t.nkeys);
+                auto tile = [&](const Ring<L::ST> &r) { return smem_u32(sm + L::OFF_RING + r.st * L::TILE); };
+                auto scores = [&](int j, Ring<L::ST> &k) -> bool {  // S of key tile j, into buffer (nt + j) & 1
+                    k = ring;
+                    ring.next();
+                    if (!wait1(&ring_full[k.st], k.ph)) return false;
+                    if (t.foreign && j == nn - 1 && t.nkeys % kTile) {  // dS is 0 there, but 0 * NaN is not
+                        request_clear(clear_req, clear_job, k.st, t.nkeys % kTile);
+                        if (!wait1(clean, nc++)) return false;
+                    }
                     const int sb = (nt + j) & 1;
-                    mma_dots<D>(t_s + sb * 128, qb, ring(p));
+                    tc_fence_after();
+                    mma_dots<D>(t_s + sb * 128, qb, tile(k));
                     mma_commit(&s_full[sb]);
-                }
-                return true;
-            };
-            auto dprob = [&](int j) -> bool {
-                const int p = pos + 2 * j + 1;
-                if (!wait(&ring_full[p % L::ST], p / L::ST, 22)) return false;
-                if (elect_one()) {
+                    return true;
+                };
+                auto dprob = [&](int j) -> bool {
+                    const Ring<L::ST> v = ring;
+                    ring.next();
+                    if (!wait1(&ring_full[v.st], v.ph)) return false;
+                    if (j > 0 && !wait1(dp_read, nt + j - 1)) return false;
                     tc_fence_after();
-                    mma_dots<D>(t_dp, ob, ring(p));
+                    mma_dots<D>(t_dp, ob, tile(v));
                     mma_commit(dp_full);
-                    mma_commit(&ring_empty[p % L::ST]);
+                    mma_commit(&ring_empty[v.st]);
                     if (j == nn - 1) mma_commit(fix_empty);
-                }
-                return true;
-            };
-            ok = scores(0) && dprob(0);
-            for (int j = 0; ok && j < nn; ++j) {
-                if (j + 1 < nn) {
-                    if (!(ok = scores(j + 1))) break;
-                    if (!(ok = wait(dp_read, nt + j, 22))) break;
-                    if (!(ok = dprob(j + 1))) break;
-                } else if (!(ok = wait(dp_read, nt + j, 22))) {
-                    break;
-                }
-                if (!(ok = wait(ds_full, nt + j, 22))) break;
-                if (elect_one()) {
+                    return true;
+                };
+                Ring<L::ST> k, kn;
+                ok = scores(0, k) && dprob(0);
+                for (int j = 0; ok && j < nn; ++j) {
+                    if (j + 1 < nn) {
+                        if (!(ok = scores(j + 1, kn) && dprob(j + 1))) break;
+                    } else if (!(ok = wait1(dp_read, nt + j))) {  // the next item's dP overwrites it
+                        break;
+                    }
+                    if (!(ok = wait1(ds_full, nt + j))) break;
                     tc_fence_after();
-                    const int p = pos + 2 * j;
-                    mma_sum<D, 64>(t_dq, t_s + ((nt + j) & 1) * 128, ring(p), j > 0);
-                    mma_commit(&ring_empty[p % L::ST]);
+                    mma_sum<D, 64>(t_dq, t_s + ((nt + j) & 1) * 128, tile(k), j > 0);
+                    mma_commit(&ring_empty[k.st]);
                     if (j == nn - 1) mma_commit(acc_full);
+                    k = kn;
                 }
+                nt += nn;
             }
-            pos += 2 * nn;
-            nt += nn;
-        }
-        if (!ok && elect_one()) {
-            mma_commit(done);
-            mbar_wait(done, 0, kDrainWaitNs);
+            request_clear(clear_req, clear_job, -1, 0);
+            if (!ok) {  // the MMAs issued so far end before tensor memory is freed (bounded)
+                mma_commit(done);
+                mbar_wait(done, 0, kDrainWaitNs);
+            }
         }
         __syncwarp();
+    } else if (warp == kWarpClear) {
+        clear_role(sm + L::OFF_RING, L::TILE, L::NH, clear_req, clean, clear_job, abort_flag, lane);
     } else if (warp < 8) {
         // ============================================================ dS, 64 keys per warpgroup
         const int w = warp >> 2, r = threadIdx.x & 127;
