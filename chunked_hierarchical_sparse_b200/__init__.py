@@ -14,8 +14,8 @@ lse [B, L, h_q, K].
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -134,18 +134,24 @@ def _need(t: torch.Tensor, name: str, shape, dtype=None, device=None, host_ok=Fa
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _run(name: str, dev, stream, *args):
     """Call a C entry point with the tensors' device current, on the given stream or
     else that device's current stream (the library launches on the current device)."""
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {dev}")
     fn = getattr(load_library(), name)
-    with torch.cuda.device(dev):
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        _check(fn(*args, ctypes.c_void_p(s.cuda_stream)), name)
+    if stream is None:
+        s = torch.cuda.current_stream(dev).cuda_stream
+    elif stream.device != dev:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {dev}")
+    else:
+        s = stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, s), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, s), name)
 
 
 def _check(code: int, where: str):
@@ -332,11 +338,23 @@ def hsa_bwd(q, k, v, q_slc, dO, lse, idx, w, kbar, K: int, S: int = 64, ws=None,
 def _allocating(dev, stream):
     """Allocate outputs and workspace on the stream that the call runs on: their memory
     is then not in use by another stream's earlier work, nor reused before the call ends."""
-    if stream is None:
-        return contextlib.nullcontext()
     if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
     return torch.cuda.stream(stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def _prompt_shape(B, L, h_q, h_kv, d, n_seq, off_by_one, dtype):
+    """The C struct of a shape and its workspace bytes, forward and backward."""
+    sh = HsaPromptShape(B, L, h_q, h_kv, d, n_seq, off_by_one, dtype)
+    lib = load_library()
+    return ctypes.byref(sh), *(int(lib.hsa_prompt_workspace_size(ctypes.byref(sh), op)) for op in (OP_FWD, OP_BWD))
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefix_shape(*fields):
+    sh = HsaPrefixShape(*fields)
+    return ctypes.byref(sh), int(load_library().hsa_prefix_workspace_size(ctypes.byref(sh)))
 
 
 def _out(t, name, shape, dtype, dev):
@@ -346,7 +364,7 @@ def _out(t, name, shape, dtype, dev):
     return t
 
 
-def _prompt_shape(q, k, v, cu_seqlens, off_by_one):
+def _prompt_args(q, k, v, cu_seqlens, off_by_one):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B, L, h_q, d] tensor")
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
@@ -362,22 +380,16 @@ def _prompt_shape(q, k, v, cu_seqlens, off_by_one):
         if n_seq < 1 or B != 1:
             raise ValueError("cu_seqlens: at least two entries, with every sequence packed into one batch row (B = 1)")
         _need(cu_seqlens, "cu_seqlens", (n_seq + 1,), torch.int32, dev)
-    return HsaPromptShape(B, L, h_q, h_kv, d, n_seq, 1 if off_by_one else 0, dt)
+    return _prompt_shape(B, L, h_q, h_kv, d, n_seq, 1 if off_by_one else 0, dt)
 
 
 def hsa_prompt_workspace_size(B, L, h_q, h_kv, d, dtype, op, n_seq: int = 0) -> int:
-    sh = HsaPromptShape(B, L, h_q, h_kv, d, n_seq, 0, _BF16 if dtype == torch.bfloat16 else _F32)
-    n = int(load_library().hsa_prompt_workspace_size(ctypes.byref(sh), op))
+    if op not in (OP_FWD, OP_BWD):
+        raise ValueError("op must be OP_FWD or OP_BWD")
+    n = _prompt_shape(B, L, h_q, h_kv, d, n_seq, 0, _BF16 if dtype == torch.bfloat16 else _F32)[1 if op == OP_FWD else 2]
     if n == 0:
         raise HsaError(2, "hsa_prompt_workspace_size")
     return n
-
-
-def _prompt_ws(sh, op, dev, ws):
-    n = int(load_library().hsa_prompt_workspace_size(ctypes.byref(sh), op))
-    if n == 0:
-        raise HsaError(2, "hsa_prompt_workspace_size")
-    return _workspace_bytes(n, dev, ws)
 
 
 def hsa_prompt_fwd(q, k, v, cu_seqlens=None, off_by_one: bool = False, want_lse: bool = True, o=None, lse=None,
@@ -386,40 +398,45 @@ def hsa_prompt_fwd(q, k, v, cu_seqlens=None, off_by_one: bool = False, want_lse:
     row is one prompt, or (B = 1) cu_seqlens (int32, on the GPU) gives the bounds of the
     prompts packed into it.  Returns (o, lse); rows outside every prompt keep what o and
     lse held (a tensor that the call allocates is not initialised there)."""
-    sh = _prompt_shape(q, k, v, cu_seqlens, off_by_one)
-    B, L, h_q, _ = q.shape
+    if stream is not None:
+        with _allocating(q.device, stream):
+            return hsa_prompt_fwd(q, k, v, cu_seqlens, off_by_one, want_lse, o, lse, ws)
+    sh, n, _ = _prompt_args(q, k, v, cu_seqlens, off_by_one)
+    if n == 0:
+        raise HsaError(2, "hsa_prompt_fwd")
     dev = q.device
-    with _allocating(dev, stream):
-        o = _out(o, "o", q.shape, q.dtype, dev)
-        if lse is not None or want_lse:
-            lse = _out(lse, "lse", (B, L, h_q), torch.float32, dev)
-        w_, n = _prompt_ws(sh, OP_FWD, dev, ws)
-        _run("hsa_prompt_fwd", dev, stream, ctypes.byref(sh), _p(q), _p(k), _p(v), _p(cu_seqlens), _p(o), _p(lse),
-             _p(w_), n)
+    o = _out(o, "o", q.shape, q.dtype, dev)
+    if lse is not None or want_lse:
+        lse = _out(lse, "lse", q.shape[:3], torch.float32, dev)
+    w_, n = _workspace_bytes(n, dev, ws)
+    _run("hsa_prompt_fwd", dev, None, sh, _p(q), _p(k), _p(v), _p(cu_seqlens), _p(o), _p(lse), _p(w_), n)
     return o, lse
 
 
 def hsa_prompt_bwd(q, k, v, o, dO, lse, cu_seqlens=None, dq=None, dk=None, dv=None, ws=None, stream=None):
     """Backward of hsa_prompt_fwd (o and lse as it returned them, with or without
     off_by_one).  Returns (dq, dk, dv); rows outside every prompt as in the forward."""
-    sh = _prompt_shape(q, k, v, cu_seqlens, False)
+    if stream is not None:
+        with _allocating(q.device, stream):
+            return hsa_prompt_bwd(q, k, v, o, dO, lse, cu_seqlens, dq, dk, dv, ws)
+    sh, _, n = _prompt_args(q, k, v, cu_seqlens, False)
+    if n == 0:
+        raise HsaError(2, "hsa_prompt_bwd")
     dev = q.device
     _need(o, "o", q.shape, q.dtype, dev)
     _need(dO, "dO", q.shape, q.dtype, dev)
     _need(lse, "lse", q.shape[:3], torch.float32, dev)
-    with _allocating(dev, stream):
-        dq = _out(dq, "dq", q.shape, q.dtype, dev)
-        dk = _out(dk, "dk", k.shape, q.dtype, dev)
-        dv = _out(dv, "dv", v.shape, q.dtype, dev)
-        w_, n = _prompt_ws(sh, OP_BWD, dev, ws)
-        _run("hsa_prompt_bwd", dev, stream, ctypes.byref(sh), _p(q), _p(k), _p(v), _p(o), _p(dO), _p(lse),
-             _p(cu_seqlens), _p(dq), _p(dk), _p(dv), _p(w_), n)
+    dq = _out(dq, "dq", q.shape, q.dtype, dev)
+    dk = _out(dk, "dk", k.shape, q.dtype, dev)
+    dv = _out(dv, "dv", v.shape, q.dtype, dev)
+    w_, n = _workspace_bytes(n, dev, ws)
+    _run("hsa_prompt_bwd", dev, None, sh, _p(q), _p(k), _p(v), _p(o), _p(dO), _p(lse), _p(cu_seqlens), _p(dq),
+         _p(dk), _p(dv), _p(w_), n)
     return dq, dk, dv
 
 
 def hsa_prefix_workspace_size(B, P, cap, h_q, h_kv, d, dtype) -> int:
-    sh = HsaPrefixShape(B, P, cap, h_q, h_kv, d, 0, _BF16 if dtype == torch.bfloat16 else _F32, P * d)
-    n = int(load_library().hsa_prefix_workspace_size(ctypes.byref(sh)))
+    n = _prefix_shape(B, P, cap, h_q, h_kv, d, 0, _BF16 if dtype == torch.bfloat16 else _F32, P * d)[1]
     if n == 0:
         raise HsaError(2, "hsa_prefix_workspace_size")
     return n
@@ -446,6 +463,9 @@ def hsa_prefix_decode(q, k_prefix, v_prefix, k_cache, v_cache, lens, off_by_one:
     k_prefix, v_prefix [h_kv,P,d] (for example the first P tokens of one prompt's k[0],
     v[0] in hsa_prompt_fwd); k_cache, v_cache [B,h_kv,cap,d] with the lens[b] (int32, on
     the GPU) tokens that sequence b has of its own.  Returns (o, lse)."""
+    if stream is not None:
+        with _allocating(q.device, stream):
+            return hsa_prefix_decode(q, k_prefix, v_prefix, k_cache, v_cache, lens, off_by_one, want_lse, o, lse, ws)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [B, h_q, d] tensor")
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
@@ -460,17 +480,15 @@ def hsa_prefix_decode(q, k_prefix, v_prefix, k_cache, v_cache, lens, off_by_one:
     stride = _prefix_planes(k_prefix, "k_prefix", h_kv, d, q.dtype, dev)
     if v_prefix.shape != k_prefix.shape or _prefix_planes(v_prefix, "v_prefix", h_kv, d, q.dtype, dev) != stride:
         raise ValueError("v_prefix must have k_prefix's shape and strides")
-    sh = HsaPrefixShape(B, k_prefix.shape[1], cap, h_q, h_kv, d, 1 if off_by_one else 0, dt, stride)
-    n = int(load_library().hsa_prefix_workspace_size(ctypes.byref(sh)))
+    sh, n = _prefix_shape(B, k_prefix.shape[1], cap, h_q, h_kv, d, 1 if off_by_one else 0, dt, stride)
     if n == 0:
-        raise HsaError(2, "hsa_prefix_workspace_size")
-    with _allocating(dev, stream):
-        o = _out(o, "o", q.shape, q.dtype, dev)
-        if lse is not None or want_lse:
-            lse = _out(lse, "lse", (B, h_q), torch.float32, dev)
-        w_, n = _workspace_bytes(n, dev, ws)
-        _run("hsa_prefix_decode", dev, stream, ctypes.byref(sh), _p(q), _p(k_prefix), _p(v_prefix), _p(k_cache),
-             _p(v_cache), _p(lens), _p(o), _p(lse), _p(w_), n)
+        raise HsaError(2, "hsa_prefix_decode")
+    o = _out(o, "o", q.shape, q.dtype, dev)
+    if lse is not None or want_lse:
+        lse = _out(lse, "lse", (B, h_q), torch.float32, dev)
+    w_, n = _workspace_bytes(n, dev, ws)
+    _run("hsa_prefix_decode", dev, None, sh, _p(q), _p(k_prefix), _p(v_prefix), _p(k_cache), _p(v_cache), _p(lens),
+         _p(o), _p(lse), _p(w_), n)
     return o, lse
 
 

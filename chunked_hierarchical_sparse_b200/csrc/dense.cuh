@@ -7,6 +7,8 @@
 // [.., token, head, d] makes such a tile one box of consecutive memory per token.
 #pragma once
 
+#include <utility>
+
 #include "hsa_internal.cuh"
 
 namespace hsa {
@@ -30,10 +32,10 @@ struct Args {
     int cap;                     // tokens of a sequence's own cache
     const int32_t *lens;         // [B]
     // The prefix is cut into pre_slots slots of pre_sub keys, each own cache into suf_slots
-    // of suf_sub; a slot's attention is one partial.  An item takes `per` slots at a time
-    // (one per stream of the tensor-core kernel, where the streams split the keys).
-    int pre_tiles, pre_sub, pre_slots, pre_per;
-    int suf_sub, suf_slots, suf_per;
+    // of suf_sub; an item takes one slot, whose attention is one partial.
+    int pre_tiles, pre_sub, pre_slots;
+    int suf_sub, suf_slots;
+    int split;                   // tensor cores: a prefix item's two streams split its keys (its rows otherwise)
     // tensors: 0 = the prompt's (or the prefix's) keys and values, 1 = the own caches'
     const void *q, *k[2], *v[2];
     int64_t plane[2];            // elements between two (batch, group) planes of k[i] / v[i]
@@ -51,7 +53,7 @@ struct Item {
     int plane;        // (batch, group) plane of k / v
     int key0, nkeys;  // first key and number of keys
     int off;          // row of token i sees key j (both relative) iff j <= off + i
-    int slot;         // decode: (first) partial slot
+    int slot;         // decode: partial slot
     int foreign;      // the last tile of 128 keys reaches beyond this sequence's own
 };
 
@@ -62,15 +64,11 @@ __device__ __forceinline__ int own_len(const Args &a, int b) {
     return min(max(n, 0), a.cap);
 }
 
-__host__ __device__ __forceinline__ int pre_items(const Args &a) {
-    return a.pre_slots ? (a.pre_slots + a.pre_per - 1) / a.pre_per : 0;
-}
-__host__ __device__ __forceinline__ int suf_items(const Args &a) {
-    return a.suf_slots ? (a.suf_slots + a.suf_per - 1) / a.suf_per : 0;
-}
+__host__ __device__ __forceinline__ int pre_items(const Args &a) { return a.hkv * a.pre_tiles * a.pre_slots; }
+__host__ __device__ __forceinline__ int suf_items(const Args &a) { return a.hkv * a.B * a.suf_slots; }
 
 __device__ __forceinline__ int item_count(const Args &a) {
-    if (a.decode) return a.hkv * (a.pre_tiles * pre_items(a) + a.B * suf_items(a));
+    if (a.decode) return pre_items(a) + suf_items(a);
     return a.plan ? *a.plan_n * a.hkv : a.B * a.hkv * a.tiles;
 }
 
@@ -102,31 +100,58 @@ __device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
     }
     it.off = kNoMask;
     it.foreign = 1;
-    const int npre = a.hkv * a.pre_tiles * pre_items(a);
-    if (i < npre) {
-        it.g = i % a.hkv;
-        const int r = i / a.hkv, tile = r % a.pre_tiles, s = r / a.pre_tiles;
+    // the two kinds alternate in proportion, so that the prefix's products (many rows per
+    // key) run beside the own caches' reads (few rows per key)
+    const int64_t np = pre_items(a), all = np + suf_items(a);
+    const int before = (int)(i * np / all);  // prefix items among the first i
+    if ((int)((i + 1) * np / all) > before) {
+        it.g = before % a.hkv;
+        const int r = before / a.hkv, tile = r % a.pre_tiles;
+        it.slot = r / a.pre_tiles;
         it.tok0 = tile * a.tok;
         it.ntok = min(a.tok, a.B - it.tok0);
         it.src = 0;
         it.plane = it.g;
-        it.slot = s * a.pre_per;
         it.key0 = it.slot * a.pre_sub;
-        it.nkeys = min(a.pre_per * a.pre_sub, a.L - it.key0);
+        it.nkeys = min(a.pre_sub, a.L - it.key0);
     } else {
-        i -= npre;
+        i -= before;
         it.g = i % a.hkv;
-        const int r = i / a.hkv;
+        const int r = i / a.hkv, s = r / a.B;
         it.tok0 = r % a.B;
         it.ntok = 1;
-        const int s = r / a.B;
         it.src = 1;
         it.plane = it.tok0 * a.hkv + it.g;
-        it.slot = a.pre_slots + s * a.suf_per;
-        it.key0 = s * a.suf_per * a.suf_sub;
-        it.nkeys = min(a.suf_per * a.suf_sub, own_len(a, it.tok0) - it.key0);
+        it.slot = a.pre_slots + s;
+        it.key0 = s * a.suf_sub;
+        it.nkeys = min(a.suf_sub, own_len(a, it.tok0) - it.key0);
     }
     return it.ntok > 0 && it.nkeys > 0;
+}
+
+// ------------------------------------------------------------------ launches
+// A call's kernels run one behind the other on its stream.  Each but the first is
+// launched so that its blocks may start while the kernel before it drains: it does
+// its own set-up, then waits (dependency_wait, executed by every thread that reads or
+// writes global memory) until that kernel is complete and its results are visible.
+// A kernel lets the next one start by dependents_may_start (or by ending).
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_next(bool behind_kernel, void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t st,
+                        A &&...args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = behind_kernel ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kernel, std::forward<A>(args)...);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -134,8 +159,9 @@ __device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
 // (first_dear: the cost of a sequence's tiles falls with their index -- the tiles
 // of keys of the backward -- instead of rising).  A cu_seqlens that does not rise
 // inside [0, L] is reported and gives no tiles.
+// The first of a call's launches (`clear`) also zeroes the workspace header.
 cudaError_t launch_plan(const int32_t *cu, int n_seq, int L, int tok, bool first_dear, int4 *plan, int32_t *plan_n,
-                        DevStatus *ds, cudaStream_t st);
+                        DevStatus *ds, bool clear, cudaStream_t st);
 inline int64_t plan_cap(int L, int n_seq, int tok) { return (int64_t)L / tok + n_seq; }
 
 struct BwdArgs {

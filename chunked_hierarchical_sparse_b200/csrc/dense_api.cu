@@ -123,7 +123,7 @@ hsa_status_t check_prompt_call(const hsa_prompt_shape_t *shape, const int32_t *c
 constexpr int kSms = 148;
 
 struct PrefixPlan {
-    int tok, pre_tiles, pre_sub, pre_slots, pre_per, suf_sub, suf_slots, suf_per;
+    int tok, split, pre_tiles, pre_sub, pre_slots, suf_sub, suf_slots;
     size_t po, plse, bytes;  // workspace offsets
 };
 
@@ -140,7 +140,7 @@ hsa_status_t check_prefix(const hsa_prefix_shape_t *s) {
 }
 
 // keys per slot: about `want` slots in all for `jobs` independent jobs of `keys` keys, in whole tiles
-int split(int64_t keys, int64_t jobs, int64_t want, int tile) {
+int slot_keys(int64_t keys, int64_t jobs, int64_t want, int tile) {
     if (keys == 0) return 0;
     const int64_t n = std::clamp<int64_t>(want / std::max<int64_t>(jobs, 1), 1, ceil_div(keys, tile));
     return (int)round_up(ceil_div(keys, n), tile);
@@ -149,17 +149,16 @@ int split(int64_t keys, int64_t jobs, int64_t want, int tile) {
 PrefixPlan plan_prefix(const hsa_prefix_shape_t &s) {
     PrefixPlan p{};
     const bool tc = s.dtype == HSA_BF16;
-    const int G = s.h_q / s.h_kv, keys = tc ? 128 : kSimtRows, fit = (tc ? 128 : kSimtRows) / G;
+    // a slot is worked on by two streams of 128 keys (tensor cores) or one of 64
+    const int G = s.h_q / s.h_kv, keys = tc ? 256 : kSimtRows, fit = (tc ? 128 : kSimtRows) / G;
     // tensor cores: a batch beyond one row tile shares the keys between two row tiles,
     // a smaller one (and every own cache) splits them between the two streams
-    const bool pair = tc && s.B > fit;
-    p.tok = pair ? 2 * fit : fit;
-    p.pre_per = tc && !pair ? 2 : 1;
-    p.suf_per = tc ? 2 : 1;
+    p.split = tc && s.B <= fit;
+    p.tok = tc && !p.split ? 2 * fit : fit;
     p.pre_tiles = (int)ceil_div(s.B, p.tok);
-    p.pre_sub = split(s.P, (int64_t)s.h_kv * p.pre_tiles, 2 * kSms, keys);
+    p.pre_sub = slot_keys(s.P, (int64_t)s.h_kv * p.pre_tiles, 2 * kSms, keys);
     p.pre_slots = p.pre_sub ? (int)ceil_div(s.P, p.pre_sub) : 0;
-    p.suf_sub = split(s.cap, (int64_t)s.h_kv * s.B, 2 * kSms, keys);
+    p.suf_sub = slot_keys(s.cap, (int64_t)s.h_kv * s.B, 2 * kSms, keys);
     p.suf_slots = p.suf_sub ? (int)ceil_div(s.cap, p.suf_sub) : 0;
     Carver c{nullptr};
     const size_t rows = (size_t)s.B * s.h_q * (p.pre_slots + p.suf_slots);
@@ -187,14 +186,15 @@ hsa_status_t hsa_prompt_fwd(const hsa_prompt_shape_t *shape, const void *q, cons
     if (s != HSA_OK) return s;
     if (!empty && (!all_ok({q, k, v, o}) || !opt_ok(lse))) return HSA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeader, st);
+    // the first kernel of a packed call clears the header itself
+    cudaError_t e = empty || !cu_seqlens ? cudaMemsetAsync(ws, 0, kWsHeader, st) : cudaSuccess;
     if (empty || e != cudaSuccess) return cuda_status(e);
     const PromptWs w = carve_prompt(*shape, ws, false);
     Args a = prompt_args(*shape, q, k, v, ws, w, row_tile(*shape));
     a.o = o;
     a.lse = lse;
     TimedLaunch tl(HSA_K_PROMPT_FWD, cu_seqlens ? 2 : 1, st);
-    if (cu_seqlens) e = launch_plan(cu_seqlens, shape->n_seq, shape->L, a.tok, false, w.plan, word(ws, kWordPlanN), a.ds, st);
+    if (cu_seqlens) e = launch_plan(cu_seqlens, shape->n_seq, shape->L, a.tok, false, w.plan, word(ws, kWordPlanN), a.ds, true, st);
     if (e == cudaSuccess) {
         const int64_t items = max_items(*shape, a.tok);
         e = shape->dtype == HSA_BF16 ? launch_fwd_tc(a, shape->d, items, word(ws, kWordNext), st)
@@ -211,7 +211,8 @@ hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, cons
     if (s != HSA_OK) return s;
     if (!empty && !all_ok({q, k, v, o, dO, lse, dq, dk, dv})) return HSA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeader, st);
+    // the first kernel of a packed call clears the header itself
+    cudaError_t e = empty || !cu_seqlens ? cudaMemsetAsync(ws, 0, kWsHeader, st) : cudaSuccess;
     if (empty || e != cudaSuccess) return cuda_status(e);
     const PromptWs w = carve_prompt(*shape, ws, true);
     const bool bf16 = shape->dtype == HSA_BF16;
@@ -224,9 +225,9 @@ hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, cons
     b.dq = dq; b.dk = dk; b.dv = dv;
     TimedLaunch tl(HSA_K_PROMPT_BWD, cu_seqlens ? 5 : 3, st);
     if (cu_seqlens) {
-        e = launch_plan(cu_seqlens, shape->n_seq, shape->L, b.a.tok, false, w.plan, word(ws, kWordPlanN), b.a.ds, st);
+        e = launch_plan(cu_seqlens, shape->n_seq, shape->L, b.a.tok, false, w.plan, word(ws, kWordPlanN), b.a.ds, true, st);
         if (e == cudaSuccess)
-            e = launch_plan(cu_seqlens, shape->n_seq, shape->L, bwd_key_tile(*shape), true, w.kplan, word(ws, kWordKPlanN), b.a.ds, st);
+            e = launch_plan(cu_seqlens, shape->n_seq, shape->L, bwd_key_tile(*shape), true, w.kplan, word(ws, kWordKPlanN), b.a.ds, false, st);
     }
     if (e == cudaSuccess) e = launch_delta(b, shape->d, bf16, st);
     if (e == cudaSuccess) {
@@ -267,8 +268,9 @@ hsa_status_t hsa_prefix_decode(const hsa_prefix_shape_t *shape, const void *q, c
     a.scale = 1.0f / sqrtf((float)shape->d);
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)shape->d));
     a.cap = shape->cap; a.lens = lens;
-    a.pre_tiles = p.pre_tiles; a.pre_sub = p.pre_sub; a.pre_slots = p.pre_slots; a.pre_per = p.pre_per;
-    a.suf_sub = p.suf_sub; a.suf_slots = p.suf_slots; a.suf_per = p.suf_per;
+    a.split = p.split;
+    a.pre_tiles = p.pre_tiles; a.pre_sub = p.pre_sub; a.pre_slots = p.pre_slots;
+    a.suf_sub = p.suf_sub; a.suf_slots = p.suf_slots;
     a.q = q;
     a.k[0] = k_prefix; a.v[0] = v_prefix; a.plane[0] = shape->prefix_stride;
     a.k[1] = k_cache; a.v[1] = v_cache; a.plane[1] = (int64_t)shape->cap * shape->d;
@@ -276,7 +278,7 @@ hsa_status_t hsa_prefix_decode(const hsa_prefix_shape_t *shape, const void *q, c
     a.po = reinterpret_cast<float *>(static_cast<char *>(ws) + p.po);
     a.plse = reinterpret_cast<float *>(static_cast<char *>(ws) + p.plse);
     a.ds = static_cast<DevStatus *>(ws);
-    const int64_t items = (int64_t)a.hkv * ((int64_t)a.pre_tiles * pre_items(a) + (int64_t)a.B * suf_items(a));
+    const int64_t items = (int64_t)pre_items(a) + suf_items(a);
     TimedLaunch tl(HSA_K_PREFIX, items > 0 ? 2 : 1, st);
     if (items > 0)
         e = bf16 ? launch_fwd_tc(a, shape->d, items, word(ws, kWordNext), st)

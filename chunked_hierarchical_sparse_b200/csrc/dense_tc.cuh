@@ -195,12 +195,12 @@ template <int N> __device__ __forceinline__ void reg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// ------------------------------------------------------------------ tensor maps (host)
+// ------------------------------------------------------------------ launches (host)
+int sm_count();  // of the current device
 // bf16, 64-column boxes of `b1` x `b2` rows, 128-byte swizzle: [n2][n1][cols] with
 // strides s1 and s2 in elements
 bool make_map3(CUtensorMap *m, const void *base, uint64_t cols, uint64_t n1, uint64_t s1, uint64_t n2, uint64_t s2,
                uint32_t b1, uint32_t b2);
-bool tensor_maps_available();
 
 }  // namespace dense
 }  // namespace hsa

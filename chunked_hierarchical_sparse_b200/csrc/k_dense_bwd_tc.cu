@@ -19,6 +19,8 @@
 // Two compute warpgroups take half of a tile's columns each (64 values of S and of dP
 // per thread); the MMAs are issued so that one warpgroup step always has one or two
 // products running behind it.
+#include <algorithm>
+
 #include "dense_tc.cuh"
 
 namespace hsa {
@@ -139,6 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
+    dependency_wait();
+    dependents_may_start();
     const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + D;
     auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
     // row tiles of an item: from the one that holds its first key's token to the sequence's end
@@ -417,6 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
+    dependency_wait();
+    dependents_may_start();
     const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;  // S: two buffers
     auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
     auto tiles = [](int keys) { return (keys + kTile - 1) / kTile; };
@@ -631,16 +637,12 @@ cudaError_t launch(const BwdArgs &b, int64_t row_items, int64_t key_items, int32
         return cudaErrorInvalidValue;
     cudaError_t e = set_smem_once((const void *)bwd_key_tc_kernel<D>, Smem<D, true>::ALLOC);
     if (e == cudaSuccess) e = set_smem_once((const void *)bwd_row_tc_kernel<D>, Smem<D, false>::ALLOC);
-    int dev = 0, sms = 0;
-    if (e == cudaSuccess) e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    bwd_key_tc_kernel<D><<<(int)(key_items < sms ? key_items : sms), kThreads, Smem<D, true>::ALLOC, st>>>(
-        mq, mo, mk, mv, b, next, wait_limit_ns());
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    bwd_row_tc_kernel<D><<<(int)(row_items < sms ? row_items : sms), kThreads, Smem<D, false>::ALLOC, st>>>(
-        mq, mo, mk, mv, b, next + 1, wait_limit_ns());
-    return cudaGetLastError();
+    e = launch_next(true, bwd_key_tc_kernel<D>, (int)std::min<int64_t>(key_items, sm_count()), kThreads,
+                    Smem<D, true>::ALLOC, st, mq, mo, mk, mv, b, next, wait_limit_ns());
+    if (e != cudaSuccess) return e;
+    return launch_next(true, bwd_row_tc_kernel<D>, (int)std::min<int64_t>(row_items, sm_count()), kThreads,
+                       Smem<D, false>::ALLOC, st, mq, mo, mk, mv, b, next + 1, wait_limit_ns());
 }
 
 }  // namespace

@@ -20,6 +20,9 @@
 // - Decode otherwise: both streams hold the same rows and take half of the keys each.
 // Warp 8 deals the items (dynamically, dearest first) and loads by TMA, warp 9
 // issues the MMAs.
+#include <algorithm>
+#include <atomic>
+
 #include "dense_tc.cuh"
 
 namespace hsa {
@@ -40,15 +43,16 @@ template <int D> struct Smem {
     static constexpr int OFF_Q = 0;                   // [2]
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_ITEM = OFF_KV + ST * TILE;
-    static constexpr int OFF_BAR = OFF_ITEM + kItems * 128;
+    static constexpr int OFF_JOINT = OFF_ITEM + kItems * 128;  // m and l of stream 1's rows
+    static constexpr int OFF_BAR = OFF_JOINT + 1024;
     static constexpr int OFF_MISC = OFF_BAR + 512;
     static constexpr int ALLOC = OFF_MISC + 64 + 1024;  // + alignment to 1 KB
 };
 static_assert(Smem<128>::ALLOC <= 232448 && Smem<64>::ALLOC <= 232448, "shared memory of a CTA");
 
 struct TcItem {
-    int end, src, plane, g, one, shared, foreign;  // one: load the single token's rows only
-    int tok[2], ntok[2], key0[2], nkeys[2], off[2], slot[2];
+    int end, src, plane, g, one, shared, foreign, slot;  // one: load the single token's rows only
+    int tok[2], ntok[2], key0[2], nkeys[2], off[2];
 };
 static_assert(sizeof(TcItem) <= 128, "item ring");
 
@@ -56,10 +60,10 @@ static_assert(sizeof(TcItem) <= 128, "item ring");
 __device__ __forceinline__ bool get_tc_item(const Args &a, int i, TcItem &t) {
     Item it;
     const bool some = get_item(a, i, it);
-    const int tt = a.decode ? (it.slot >= a.pre_slots ? 1 : 128 / a.G) : a.tok / 2;  // tokens of one stream's tile
+    const int tt = a.decode ? 128 / a.G : a.tok / 2;  // tokens of one stream's tile (shared keys)
     t.end = 0; t.src = it.src; t.plane = it.plane; t.g = it.g; t.one = 0;
-    t.shared = !a.decode || (it.src == 0 && a.pre_per == 1);
-    t.foreign = it.foreign;
+    t.shared = !a.decode || (it.src == 0 && !a.split);
+    t.foreign = it.foreign; t.slot = it.slot;
     if (t.shared) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -68,19 +72,17 @@ __device__ __forceinline__ bool get_tc_item(const Args &a, int i, TcItem &t) {
             t.key0[s] = it.key0;
             t.off[s] = it.off == kNoMask ? kNoMask : it.off + s * tt;
             t.nkeys[s] = t.ntok[s] <= 0 ? 0 : (it.off == kNoMask ? it.nkeys : min(it.nkeys, t.off[s] + t.ntok[s]));
-            t.slot[s] = it.slot;
         }
-    } else {  // the item's keys are two slots, one per stream
-        const int sub = it.src ? a.suf_sub : a.pre_sub;
+    } else {  // half of the keys each, in whole tiles
+        const int half = ((it.nkeys + 2 * kKeys - 1) / (2 * kKeys)) * kKeys;
         t.one = it.src;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             t.tok[s] = it.tok0;
             t.ntok[s] = it.ntok;
-            t.key0[s] = it.key0 + s * sub;
+            t.key0[s] = it.key0 + s * half;
             t.off[s] = kNoMask;
-            t.nkeys[s] = max(0, min(sub, it.nkeys - s * sub));
-            t.slot[s] = it.slot + s;
+            t.nkeys[s] = max(0, min(half, it.nkeys - s * half));
         }
     }
     return some;
@@ -115,11 +117,12 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     TcItem *items = reinterpret_cast<TcItem *>(sm + L::OFF_ITEM);
+    float *joint = reinterpret_cast<float *>(sm + L::OFF_JOINT);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
     uint64_t *item_full = bar, *item_empty = bar + kItems;
     uint64_t *q_full = item_empty + kItems, *q_empty = q_full + 2;
     uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2;
-    uint64_t *p_half = o_full + 2, *clean = p_half + 2, *clear_req = clean + 1, *done = clear_req + 1;
+    uint64_t *p_half = o_full + 2, *clean = p_half + 2, *clear_req = clean + 1, *join_full = clear_req + 1, *join_empty = join_full + 1, *done = join_empty + 1;
     uint64_t *kv_full = done + 1, *kv_empty = kv_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
@@ -132,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1); mbar_init(&p_half[i], 4); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1);
         }
+        mbar_init(join_full, 4); mbar_init(join_empty, 4);
         mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1); }
         *abort_flag = 0;
@@ -148,6 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
+    dependency_wait();
+    dependents_may_start();
     auto wait = [&](uint64_t *b, uint32_t par, int role) { return warp_wait(b, par & 1, wait_ns, abort_flag, a.ds, role); };
     auto tiles = [](int keys) { return (keys + kKeys - 1) / kKeys; };
 
@@ -331,13 +337,14 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
         const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256 + s * D;
         const int rt = r / a.G, rh = r % a.G;
         const float c = a.scale_log2;
-        int ns_done = 0, no_done = 0;
+        int ns_done = 0, no_done = 0, n_join = 0;
         bool ok = true;
         for (int n = 0; ok; ++n) {
             const int ib = n % kItems;
             if (!(ok = wait(&item_full[ib], n / kItems, 3))) break;
             const int end = items[ib].end, g = items[ib].g, tok = items[ib].tok[s], ntok = items[ib].ntok[s],
-                      nkeys = items[ib].nkeys[s], off = items[ib].off[s], slot = items[ib].slot[s];
+                      nkeys = items[ib].nkeys[s], off = items[ib].off[s], slot = items[ib].slot;
+            const bool merge = !items[ib].shared && items[ib].nkeys[1] > 0;  // both streams hold parts of the same rows
             __syncwarp();
             mbar_arrive_lane0(&item_empty[ib], lane);
             if (end) break;
@@ -466,34 +473,64 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             }
             if (!ok || !(ok = wait(&o_full[s], no_done, 3))) break;
             ++no_done;
-            if (!warp_rows) continue;
             tc_fence_after();
+            // Streams that split the keys of the same rows: stream 1 hands over m and l, stream 0 reads
+            // both O (a warp reaches its 32 rows in every column) and writes one joint result.
+            float f1 = 0.f;
+            if (merge && s == 1) {
+                joint[r] = m;
+                joint[128 + r] = l;
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_lane0(join_full, lane);
+                if (!(ok = wait(join_empty, n_join++, 3))) break;
+                continue;
+            }
+            float z = l, f = 1.f, mm = m == -INFINITY ? 0.f : m;
+            if (merge) {
+                if (!(ok = wait(join_full, n_join++, 3))) break;
+                tc_fence_after();
+                const float m1 = joint[r], top = fmaxf(m, m1);
+                mm = top == -INFINITY ? 0.f : top;
+                f = ex2(m - mm);
+                f1 = ex2(m1 - mm);
+                z = l * f + joint[128 + r] * f1;
+            }
             const bool real = r < ntok * a.G;
             const int64_t row = ((int64_t)tok + rt) * a.hq + g * a.G + rh;
-            float z = l, f = 1.f, mm = m == -INFINITY ? 0.f : m;
             if (!a.decode && a.off_by_one) {  // the added 1 is a logit of 0
                 const float top = fmaxf(mm, 0.f);
                 f = ex2(mm - top);
                 z = l * f + ex2(-top);
                 mm = top;
             }
-            const float inv = z > 0.f ? f / z : (z == 0.f ? 0.f : z);  // NaN stays NaN
+            const float inv = z > 0.f ? f / z : (z == 0.f ? 0.f : z), inv1 = merge && z > 0.f ? f1 / z : 0.f;  // NaN stays NaN
             const float lse = (mm + log2f(z)) * kLn2;
             const int64_t prow = (int64_t)slot * a.B * a.hq + row;
-            if (real) {
+            if (warp_rows && real) {
                 if (a.decode) a.plse[prow] = lse;
                 else if (a.lse) a.lse[row] = lse;
             }
 #pragma unroll
             for (int h = 0; h < D / 32; ++h) {
+                if (!warp_rows) break;
                 float y[32];
                 tmem_ld32(to + h * 32, y);
-                tmem_wait_ld();
-                if (real && a.decode) {
+                wait_loads(y);
+                if (a.decode) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[i] *= inv;
+                    if (merge) {
+                        float y1[32];
+                        tmem_ld32(to + D + h * 32, y1);
+                        wait_loads(y1);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) y[i] += y1[i] * inv1;
+                    }
                     float4 *p = reinterpret_cast<float4 *>(a.po + prow * D + h * 32);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        p[i] = make_float4(y[4 * i] * inv, y[4 * i + 1] * inv, y[4 * i + 2] * inv, y[4 * i + 3] * inv);
+                        if (real) p[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
                 } else if (real) {
                     uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row * D + h * 32);
 #pragma unroll
@@ -506,6 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                 __syncwarp();
             }
             tc_fence_before();
+            if (merge) {
+                __syncwarp();
+                mbar_arrive_lane0(join_empty, lane);
+            }
         }
     }
     tc_fence_before();
@@ -518,27 +559,25 @@ template <int D>
 cudaError_t launch(const Args &a, int64_t items, int32_t *next, cudaStream_t st) {
     CUtensorMap mq, mq1, mk[2], mv[2];
     const uint64_t rows = (uint64_t)a.B * (a.decode ? 1 : a.L), tt = 128 / a.G;
-    bool ok = make_map3(&mq, a.q, D, a.hq, D, rows, (uint64_t)a.hq * D, a.G, (uint32_t)tt) &&
-              make_map3(&mq1, a.q, D, a.hq, D, rows, (uint64_t)a.hq * D, a.G, 1);
+    bool ok = make_map3(&mq, a.q, D, a.hq, D, rows, (uint64_t)a.hq * D, a.G, (uint32_t)tt);
+    const bool have[2] = {a.L > 0, a.decode && a.cap > 0};
     for (int i = 0; ok && i < 2; ++i) {
-        const uint64_t n = i ? a.cap : a.L, planes = i ? (uint64_t)a.B * a.hkv : (a.decode ? a.hkv : (uint64_t)a.B * a.hkv);
-        if (n == 0 || !a.k[i]) continue;
+        if (!have[i]) continue;
+        const uint64_t n = i ? a.cap : a.L, planes = a.decode && !i ? a.hkv : (uint64_t)a.B * a.hkv;
         ok = make_map3(&mk[i], a.k[i], D, n, D, planes, a.plane[i], kKeys, 1) &&
              make_map3(&mv[i], a.v[i], D, n, D, planes, a.plane[i], kKeys, 1);
     }
+    // maps that no item reads through
+    if (have[1]) ok = ok && make_map3(&mq1, a.q, D, a.hq, D, rows, (uint64_t)a.hq * D, a.G, 1);
+    else mq1 = mq, mk[1] = mk[0], mv[1] = mv[0];
+    if (!have[0]) mk[0] = mk[1], mv[0] = mv[1];
     if (!ok) return cudaErrorInvalidValue;
-    const bool have0 = a.L > 0, have1 = a.decode && a.cap > 0;
-    if (!have0) { mk[0] = mk[1]; mv[0] = mv[1]; }  // never read
-    if (!have1) { mk[1] = mk[0]; mv[1] = mv[0]; }
     const size_t smem = Smem<D>::ALLOC;
-    cudaError_t e = set_smem_once((const void *)fwd_tc_kernel<D>, smem);
-    int dev = 0, sms = 0;
-    if (e == cudaSuccess) e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const cudaError_t e = set_smem_once((const void *)fwd_tc_kernel<D>, smem);
     if (e != cudaSuccess) return e;
-    const int grid = (int)(items < sms ? items : sms);
-    fwd_tc_kernel<D><<<grid, kThreads, smem, st>>>(mq, mq1, mk[0], mv[0], mk[1], mv[1], a, next, wait_limit_ns());
-    return cudaGetLastError();
+    const int grid = (int)std::min<int64_t>(items, sm_count());
+    return launch_next(a.plan != nullptr, fwd_tc_kernel<D>, grid, kThreads, smem, st, mq, mq1, mk[0], mv[0], mk[1], mv[1],
+                       a, next, wait_limit_ns());
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -559,7 +598,16 @@ EncodeTiledFn get_encode() {
 
 }  // namespace
 
-bool tensor_maps_available() { return get_encode() != nullptr; }
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep && (n = known[dev].load(std::memory_order_relaxed))) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    if (keep) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 bool make_map3(CUtensorMap *m, const void *base, uint64_t cols, uint64_t n1, uint64_t s1, uint64_t n2, uint64_t s2,
                uint32_t b1, uint32_t b2) {

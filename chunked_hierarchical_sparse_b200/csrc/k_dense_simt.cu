@@ -122,6 +122,8 @@ __global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ 
     float *Q = sm, *K = Q + kT * (D + 4), *V = K + kT * (D + 4), *P = V + kT * (D + 4);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     Item it;
+    dependency_wait();
+    dependents_may_start();
     if ((int64_t)blockIdx.x >= item_count(a) || !get_item(a, blockIdx.x, it)) return;
     const int rows = it.ntok * a.G;
     const T *q = static_cast<const T *>(a.q);
@@ -207,6 +209,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) delta_kernel(const T *o, const T *dO, float *delta, int64_t rows) {
     const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
+    dependency_wait();
+    dependents_may_start();
     if (r >= rows) return;
     float s = 0.f;
 #pragma unroll
@@ -228,6 +232,8 @@ __global__ void __launch_bounds__(kThr) bwd_dq_simt_kernel(const __grid_constant
     float *Q = sm, *G = Q + kT * (D + 4), *K = G + kT * (D + 4), *V = K + kT * (D + 4), *S = V + kT * (D + 4);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     Item it;
+    dependency_wait();
+    dependents_may_start();
     if ((int64_t)blockIdx.x >= item_count(a) || !get_item(a, blockIdx.x, it)) return;
     const int rows = it.ntok * a.G;
     const int64_t pl = it.plane * a.plane[0] + (int64_t)it.key0 * D;
@@ -287,6 +293,8 @@ __global__ void __launch_bounds__(kThr) bwd_dkv_simt_kernel(const __grid_constan
           *S = P + kT * kPS;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     KeyItem it;
+    dependency_wait();
+    dependents_may_start();
     if ((int64_t)blockIdx.x >= key_item_count(b) || !get_key_item(b, blockIdx.x, kT, it)) return;
     const int64_t pl = it.plane * a.plane[0] + (int64_t)(it.start + it.n0) * D;
     load_tile<D, T>(K, [&](int r) -> const T * { return r < it.nkeys ? static_cast<const T *>(a.k[0]) + pl + r * D : nullptr; });
@@ -346,25 +354,22 @@ template <int D> constexpr size_t dkv_smem() { return sizeof(float) * (4 * kT * 
 template <typename T, int D> cudaError_t fwd(const Args &a, int64_t items, cudaStream_t st) {
     cudaError_t e = set_smem_once((const void *)fwd_simt_kernel<T, D>, fwd_smem<D>());
     if (e != cudaSuccess) return e;
-    fwd_simt_kernel<T, D><<<(unsigned)items, kThr, fwd_smem<D>(), st>>>(a);
-    return cudaGetLastError();
+    return launch_next(a.plan != nullptr, fwd_simt_kernel<T, D>, (int)items, kThr, fwd_smem<D>(), st, a);
 }
 
 template <typename T, int D> cudaError_t delta(const BwdArgs &b, cudaStream_t st) {
     const int64_t rows = (int64_t)b.a.B * b.a.L * b.a.hq;
-    delta_kernel<T, D><<<(unsigned)ceil_div(rows, 8), 256, 0, st>>>(static_cast<const T *>(b.o),
-                                                                    static_cast<const T *>(b.dO), b.delta, rows);
-    return cudaGetLastError();
+    return launch_next(b.a.plan != nullptr, delta_kernel<T, D>, (int)ceil_div(rows, 8), 256, 0, st,
+                       static_cast<const T *>(b.o), static_cast<const T *>(b.dO), b.delta, rows);
 }
 
 template <typename T, int D> cudaError_t bwd(const BwdArgs &b, int64_t row_items, int64_t key_items, cudaStream_t st) {
     cudaError_t e = set_smem_once((const void *)bwd_dq_simt_kernel<T, D>, dq_smem<D>());
     if (e == cudaSuccess) e = set_smem_once((const void *)bwd_dkv_simt_kernel<T, D>, dkv_smem<D>());
     if (e != cudaSuccess) return e;
-    bwd_dkv_simt_kernel<T, D><<<(unsigned)key_items, kThr, dkv_smem<D>(), st>>>(b);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    bwd_dq_simt_kernel<T, D><<<(unsigned)row_items, kThr, dq_smem<D>(), st>>>(b);
-    return cudaGetLastError();
+    e = launch_next(true, bwd_dkv_simt_kernel<T, D>, (int)key_items, kThr, dkv_smem<D>(), st, b);
+    if (e != cudaSuccess) return e;
+    return launch_next(true, bwd_dq_simt_kernel<T, D>, (int)row_items, kThr, dq_smem<D>(), st, b);
 }
 
 }  // namespace
