@@ -115,6 +115,9 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _need(t: torch.Tensor, name: str, shape, dtype=None, device=None, host_ok=False):
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.is_cuda
+            and (device is None or t.device == device) and t.is_contiguous()):
+        return  # as it should be; the rest finds what is not
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if tuple(t.shape) != tuple(shape):
@@ -142,7 +145,7 @@ def _run(name: str, dev, stream, *args):
     else that device's current stream (the library launches on the current device)."""
     fn = getattr(load_library(), name)
     if stream is None:
-        s = torch.cuda.current_stream(dev).cuda_stream
+        s = torch._C._cuda_getCurrentRawStream(dev.index)  # current_stream(dev), without its wrapper object
     elif stream.device != dev:
         raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {dev}")
     else:
@@ -181,9 +184,12 @@ def _workspace_bytes(n: int, device, ws):
         if ws.numel() * ws.element_size() < n:
             raise HsaError(3, "workspace")
         return ws, ws.numel() * ws.element_size()
-    buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
-    off = (-buf.data_ptr()) % 256
-    return buf[off:off + n], n
+    buf = torch.empty(n, dtype=torch.uint8, device=device)
+    if buf.data_ptr() % 256:  # torch's allocator hands out blocks of 512 bytes; another may not
+        buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
+        off = (-buf.data_ptr()) % 256
+        buf = buf[off:off + n]
+    return buf, n
 
 
 # ------------------------------------------------------------------ entry points

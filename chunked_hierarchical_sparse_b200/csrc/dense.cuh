@@ -31,10 +31,11 @@ struct Args {
     // decode
     int cap;                     // tokens of a sequence's own cache
     const int32_t *lens;         // [B]
-    // The prefix is cut into pre_slots slots of pre_sub keys, each own cache into suf_slots
-    // of suf_sub; an item takes one slot, whose attention is one partial.
+    // The prefix is cut into pre_slots items of pre_sub keys, each own cache into suf_slots of
+    // suf_sub.  A prefix item's attention is one partial, in slot s; that of an own cache's
+    // item is suf_per partials (2: one per stream), in slots pre_slots + s suf_per + 0, 1.
     int pre_tiles, pre_sub, pre_slots;
-    int suf_sub, suf_slots;
+    int suf_sub, suf_slots, suf_per;
     int split;                   // tensor cores: a prefix item's two streams split its keys (its rows otherwise)
     // tensors: 0 = the prompt's (or the prefix's) keys and values, 1 = the own caches'
     const void *q, *k[2], *v[2];
@@ -53,7 +54,7 @@ struct Item {
     int plane;        // (batch, group) plane of k / v
     int key0, nkeys;  // first key and number of keys
     int off;          // row of token i sees key j (both relative) iff j <= off + i
-    int slot;         // decode: partial slot
+    int slot;         // decode: (first) partial slot
     int foreign;      // the last tile of 128 keys reaches beyond this sequence's own
 };
 
@@ -100,11 +101,20 @@ __device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
     }
     it.off = kNoMask;
     it.foreign = 1;
-    // the two kinds alternate in proportion, so that the prefix's products (many rows per
-    // key) run beside the own caches' reads (few rows per key)
-    const int64_t np = pre_items(a), all = np + suf_items(a);
-    const int before = (int)(i * np / all);  // prefix items among the first i
-    if ((int)((i + 1) * np / all) > before) {
+    // Prefix items (dear: many rows per key) come first, with one own-cache item (few rows
+    // per key) behind every two of them as far as they go, so that the ones' products run
+    // beside the others' reads and the small items are left for the end.
+    const int np = pre_items(a), mixed = 3 * min(np / 2, suf_items(a));
+    int before;  // prefix items among the first i
+    bool prefix;
+    if (i < mixed) {
+        before = i / 3 * 2 + (i % 3 != 0);
+        prefix = i % 3 != 1;
+    } else {
+        before = min(np, mixed / 3 * 2 + i - mixed);
+        prefix = before < np;
+    }
+    if (prefix) {
         it.g = before % a.hkv;
         const int r = before / a.hkv, tile = r % a.pre_tiles;
         it.slot = r / a.pre_tiles;
@@ -122,12 +132,15 @@ __device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
         it.ntok = 1;
         it.src = 1;
         it.plane = it.tok0 * a.hkv + it.g;
-        it.slot = a.pre_slots + s;
+        it.slot = a.pre_slots + s * a.suf_per;
         it.key0 = s * a.suf_sub;
         it.nkeys = min(a.suf_sub, own_len(a, it.tok0) - it.key0);
     }
     return it.ntok > 0 && it.nkeys > 0;
 }
+
+// Keys of the first of two streams that split n, in whole tiles of 128.
+__host__ __device__ __forceinline__ int first_half(int n) { return (n + 255) / 256 * 128; }
 
 // ------------------------------------------------------------------ launches
 // A call's kernels run one behind the other on its stream.  Each but the first is
@@ -207,10 +220,11 @@ __device__ __forceinline__ bool get_key_item(const BwdArgs &b, int i, int keys, 
     return it.nkeys > 0;
 }
 
-// fp32, on the CUDA cores (tiles of kSimtRows rows and keys)
+// fp32, on the CUDA cores (tiles of kSimtRows rows and keys); clears the header likewise
 cudaError_t launch_fwd_simt(const Args &a, int d, int64_t items, cudaStream_t st);
 // bf16, on the tensor cores: a.tok is two row tiles (128 / G tokens each), but for a
-// decode call whose batch fits one; `next` is a zero int32, the items dealt so far.
+// decode call whose batch fits one; `next`: an int32 of the header for the items dealt.
+// The header is cleared here where no kernel before it did (a.plan is null).
 cudaError_t launch_fwd_tc(const Args &a, int d, int64_t items, int32_t *next, cudaStream_t st);
 // a.tok = 128 / G, key tiles of 128; `next`: two zero int32
 cudaError_t launch_bwd_tc(const BwdArgs &b, int d, int64_t row_items, int64_t key_items, int32_t *next, cudaStream_t st);

@@ -123,7 +123,7 @@ hsa_status_t check_prompt_call(const hsa_prompt_shape_t *shape, const int32_t *c
 constexpr int kSms = 148;
 
 struct PrefixPlan {
-    int tok, split, pre_tiles, pre_sub, pre_slots, suf_sub, suf_slots;
+    int tok, split, pre_tiles, pre_sub, pre_slots, suf_sub, suf_slots, suf_per;
     size_t po, plse, bytes;  // workspace offsets
 };
 
@@ -156,12 +156,13 @@ PrefixPlan plan_prefix(const hsa_prefix_shape_t &s) {
     p.split = tc && s.B <= fit;
     p.tok = tc && !p.split ? 2 * fit : fit;
     p.pre_tiles = (int)ceil_div(s.B, p.tok);
-    p.pre_sub = slot_keys(s.P, (int64_t)s.h_kv * p.pre_tiles, 2 * kSms, keys);
+    p.pre_sub = slot_keys(s.P, (int64_t)s.h_kv * p.pre_tiles, kSms, keys);
     p.pre_slots = p.pre_sub ? (int)ceil_div(s.P, p.pre_sub) : 0;
     p.suf_sub = slot_keys(s.cap, (int64_t)s.h_kv * s.B, 2 * kSms, keys);
     p.suf_slots = p.suf_sub ? (int)ceil_div(s.cap, p.suf_sub) : 0;
+    p.suf_per = tc ? 2 : 1;
     Carver c{nullptr};
-    const size_t rows = (size_t)s.B * s.h_q * (p.pre_slots + p.suf_slots);
+    const size_t rows = (size_t)s.B * s.h_q * (p.pre_slots + p.suf_slots * p.suf_per);
     p.po = c.off;
     c.take<float>(rows * s.d);
     p.plse = c.off;
@@ -186,9 +187,8 @@ hsa_status_t hsa_prompt_fwd(const hsa_prompt_shape_t *shape, const void *q, cons
     if (s != HSA_OK) return s;
     if (!empty && (!all_ok({q, k, v, o}) || !opt_ok(lse))) return HSA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // the first kernel of a packed call clears the header itself
-    cudaError_t e = empty || !cu_seqlens ? cudaMemsetAsync(ws, 0, kWsHeader, st) : cudaSuccess;
-    if (empty || e != cudaSuccess) return cuda_status(e);
+    if (empty) return cuda_status(cudaMemsetAsync(ws, 0, kWsHeader, st));
+    cudaError_t e = cudaSuccess;  // the first launch clears the header
     const PromptWs w = carve_prompt(*shape, ws, false);
     Args a = prompt_args(*shape, q, k, v, ws, w, row_tile(*shape));
     a.o = o;
@@ -257,8 +257,8 @@ hsa_status_t hsa_prefix_decode(const hsa_prefix_shape_t *shape, const void *q, c
             return HSA_ERR_INVALID_ARG;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeader, st);
-    if (shape->B == 0 || e != cudaSuccess) return cuda_status(e);
+    if (shape->B == 0) return cuda_status(cudaMemsetAsync(ws, 0, kWsHeader, st));
+    cudaError_t e = cudaSuccess;
     const bool bf16 = shape->dtype == HSA_BF16;
     Args a{};
     a.decode = 1;
@@ -270,7 +270,7 @@ hsa_status_t hsa_prefix_decode(const hsa_prefix_shape_t *shape, const void *q, c
     a.cap = shape->cap; a.lens = lens;
     a.split = p.split;
     a.pre_tiles = p.pre_tiles; a.pre_sub = p.pre_sub; a.pre_slots = p.pre_slots;
-    a.suf_sub = p.suf_sub; a.suf_slots = p.suf_slots;
+    a.suf_sub = p.suf_sub; a.suf_slots = p.suf_slots; a.suf_per = p.suf_per;
     a.q = q;
     a.k[0] = k_prefix; a.v[0] = v_prefix; a.plane[0] = shape->prefix_stride;
     a.k[1] = k_cache; a.v[1] = v_cache; a.plane[1] = (int64_t)shape->cap * shape->d;
@@ -283,6 +283,8 @@ hsa_status_t hsa_prefix_decode(const hsa_prefix_shape_t *shape, const void *q, c
     if (items > 0)
         e = bf16 ? launch_fwd_tc(a, shape->d, items, word(ws, kWordNext), st)
                  : launch_fwd_simt(a, shape->d, items, st);
+    else
+        e = cudaMemsetAsync(ws, 0, kWsHeader, st);
     if (e == cudaSuccess) e = launch_combine(a, shape->d, bf16, st);
     return cuda_status(e);
 }

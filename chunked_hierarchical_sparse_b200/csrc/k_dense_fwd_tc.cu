@@ -32,8 +32,10 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kKeys = 128;        // keys per tile
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpClear = 10;
-constexpr int kItems = 2;         // item ring
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpClear = 10, kWarpQ = 11;
+constexpr int kItems = 3;         // item ring
+constexpr int kOneRow = 32;       // first row of stream 1 of a one-token item (at most 16 rows): the streams'
+                                  // softmaxes are then warps of different schedulers
 constexpr float kSlack = 8.f;     // log2 of how far a tile may exceed m before it moves
 
 template <int D> struct Smem {
@@ -43,7 +45,7 @@ template <int D> struct Smem {
     static constexpr int OFF_Q = 0;                   // [2]
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_ITEM = OFF_KV + ST * TILE;
-    static constexpr int OFF_JOINT = OFF_ITEM + kItems * 128;  // m and l of stream 1's rows
+    static constexpr int OFF_JOINT = OFF_ITEM + 256;  // m and l of stream 1's rows
     static constexpr int OFF_BAR = OFF_JOINT + 1024;
     static constexpr int OFF_MISC = OFF_BAR + 512;
     static constexpr int ALLOC = OFF_MISC + 64 + 1024;  // + alignment to 1 KB
@@ -54,7 +56,7 @@ struct TcItem {
     int end, src, plane, g, one, shared, foreign, slot;  // one: load the single token's rows only
     int tok[2], ntok[2], key0[2], nkeys[2], off[2];
 };
-static_assert(sizeof(TcItem) <= 128, "item ring");
+static_assert(kItems * sizeof(TcItem) <= 256, "item ring");
 
 // Item i of the call as two streams; false when neither has rows and keys.
 __device__ __forceinline__ bool get_tc_item(const Args &a, int i, TcItem &t) {
@@ -74,8 +76,8 @@ __device__ __forceinline__ bool get_tc_item(const Args &a, int i, TcItem &t) {
             t.nkeys[s] = t.ntok[s] <= 0 ? 0 : (it.off == kNoMask ? it.nkeys : min(it.nkeys, t.off[s] + t.ntok[s]));
         }
     } else {  // half of the keys each, in whole tiles
-        const int half = ((it.nkeys + 2 * kKeys - 1) / (2 * kKeys)) * kKeys;
-        t.one = it.src;
+        const int half = first_half(it.nkeys);
+        t.one = it.src;  // its partials are not joined here: stream 1's rows are on other lanes
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             t.tok[s] = it.tok0;
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kItems; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 9); }
+        for (int i = 0; i < kItems; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 10); }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1); mbar_init(&p_half[i], 4); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1);
@@ -154,6 +156,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
     const uint32_t tmem = uniform(*tmem_slot);
     dependency_wait();
     dependents_may_start();
+    // A call of at most one item per block needs no counter and clears its header here: the
+    // other blocks report nothing but waits that ran out, seconds later.
+    if (!next && blockIdx.x == 0 && threadIdx.x == 0) *a.ds = DevStatus{};
+    if (!next) __syncthreads();
     auto wait = [&](uint64_t *b, uint32_t par, int role) { return warp_wait(b, par & 1, wait_ns, abort_flag, a.ds, role); };
     auto tiles = [](int keys) { return (keys + kKeys - 1) / kKeys; };
 
@@ -162,17 +168,21 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
         if (warp == kWarpLoad) {
             // ======================================================== items and loads
             const int total = item_count(a);
-            int idx = blockIdx.x, kv = 0, nq[2] = {0, 0};
+            int idx = blockIdx.x, kv = 0;
             bool ok = true;
             auto next_item = [&]() -> int {  // the first gridDim.x items are dealt by block index
+                if (!next) return total;     // there are no more
                 int i = 0;
                 if (lane == 0) i = atomicAdd(next, 1);
                 return __shfl_sync(0xffffffffu, i, 0) + gridDim.x;
             };
-            for (int n = 0; ok; ++n) {
-                TcItem t;
-                while (idx < total && !get_tc_item(a, idx, t)) idx = next_item();
-                if (idx >= total) t.end = 1;
+            TcItem t, ahead;  // the next item is looked up (two trips to memory) before this one's loads
+            auto look_up = [&](TcItem &x) {
+                while (idx < total && !get_tc_item(a, idx, x)) idx = next_item();
+                x.end = idx >= total;
+            };
+            look_up(t);
+            for (int n = 0; ok; ++n, t = ahead) {
                 const int ib = n % kItems;
                 if (n >= kItems && !(ok = wait(&item_empty[ib], n / kItems - 1, 1))) break;
                 if (lane == 0) {
@@ -182,20 +192,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                 __syncwarp();
                 if (t.end) break;
                 const CUtensorMap *mk = t.src ? &tm_k1 : &tm_k0, *mv = t.src ? &tm_v1 : &tm_v0;
-                auto load_q = [&](int s) -> bool {
-                    if (t.nkeys[s] == 0) return true;
-                    if (nq[s] > 0 && !wait(&q_empty[s], nq[s] - 1, 1)) return false;
-                    if (lane == 0) {
-                        const int rows = t.one ? a.G : a.G * (128 / a.G);
-                        mbar_arrive_expect_tx(&q_full[s], L::NH * rows * 128);
-#pragma unroll
-                        for (int h = 0; h < L::NH; ++h)
-                            tma_load_3d(sm + L::OFF_Q + s * L::TILE + h * 16384, t.one ? &tm_q1 : &tm_q, h * 64, t.g * a.G,
-                                        t.tok[s], &q_full[s]);
-                    }
-                    ++nq[s];
-                    return true;
-                };
                 auto load_kv = [&](const CUtensorMap *m, int key) -> bool {
                     const int st = kv % L::ST;
                     if (kv >= L::ST && !wait(&kv_empty[st], kv / L::ST - 1, 1)) return false;
@@ -209,16 +205,17 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                     return true;
                 };
                 const int n0 = tiles(t.nkeys[0]), n1 = tiles(t.nkeys[1]);
+                ok = load_kv(mk, t.key0[0]);
+                if (ok && !t.shared && n1) ok = load_kv(mk, t.key0[1]);
+                idx = next_item();
+                look_up(ahead);
                 if (t.shared) {
                     const int nn = max(n0, n1);
-                    ok = load_q(0) && load_kv(mk, t.key0[0]) && load_q(1);
                     for (int j = 0; ok && j < nn; ++j) {
                         ok = load_kv(mv, t.key0[0] + j * kKeys);
                         if (ok && j + 1 < nn) ok = load_kv(mk, t.key0[0] + (j + 1) * kKeys);
                     }
                 } else {
-                    ok = load_q(0) && load_kv(mk, t.key0[0]);
-                    if (ok && n1) ok = load_q(1) && load_kv(mk, t.key0[1]);
                     for (int j = 0; ok && j < n0; ++j) {
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
@@ -228,13 +225,41 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                         }
                     }
                 }
-                idx = next_item();
             }
             if (!ok && lane == 0) {  // the loads in flight land before the CTA goes away (bounded)
                 for (int i = max(0, kv - L::ST); i < kv; ++i) mbar_wait(&kv_full[i % L::ST], (i / L::ST) & 1, kDrainWaitNs);
+            }
+            __syncwarp();
+        } else if (warp == kWarpQ) {
+            // ======================================================== rows of Q (beside the other loads, so that
+            // the next item's keys and values are on their way before this item's Q tiles are free)
+            int nq[2] = {0, 0};
+            bool ok = true;
+            for (int n = 0; ok; ++n) {
+                const int ib = n % kItems;
+                if (!(ok = wait(&item_full[ib], n / kItems, 5))) break;
+                const TcItem t = items[ib];
+                __syncwarp();
+                mbar_arrive_lane0(&item_empty[ib], lane);
+                if (t.end) break;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (!ok || t.nkeys[s] == 0) continue;
+                    if (nq[s] > 0 && !(ok = wait(&q_empty[s], nq[s] - 1, 5))) break;
+                    if (lane == 0) {
+                        const int rows = t.one ? a.G : a.G * (128 / a.G);
+                        mbar_arrive_expect_tx(&q_full[s], L::NH * rows * 128);
+#pragma unroll
+                        for (int h = 0; h < L::NH; ++h)
+                            tma_load_3d(sm + L::OFF_Q + s * L::TILE + h * 16384 + (t.one && s ? kOneRow * 128 : 0),
+                                        t.one ? &tm_q1 : &tm_q, h * 64, t.g * a.G, t.tok[s], &q_full[s]);
+                    }
+                    ++nq[s];
+                }
+            }
+            if (!ok && lane == 0)
                 for (int s = 0; s < 2; ++s)
                     if (nq[s]) mbar_wait(&q_full[s], (nq[s] - 1) & 1, kDrainWaitNs);
-            }
             __syncwarp();
         } else if (warp == kWarpMma) {
             // ======================================================== MMA issue, a single thread
@@ -288,7 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                                 if (shared ? j + 1 < nn : more) {
                                     k = kv;
                                     kv.next();
-                                    if (!(ok = wait1(&kv_full[k.st], k.ph))) break;
                                 }
                             }
                             // values behind the last key belong to something else and may be anything:
@@ -306,7 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                             if (!(ok = wait1(&p_full[s], np[s]++))) break;
                             tc_fence_after();
                             mma_sum<D, 32, 4, 8>(t_o, t_s, vs, 1);
-                            if (more) {
+                            if (last_reader(s, j)) mma_commit(&kv_empty[v.st]);
+                            if (more) {  // (the wait hides behind the products just issued)
+                                if (!(ok = wait1(&kv_full[k.st], k.ph))) break;
+                                tc_fence_after();
                                 mma_dots<D>(t_s, smem_u32(sm + L::OFF_Q + s * L::TILE), smem_u32(sm + L::OFF_KV + k.st * L::TILE));
                                 mma_commit(&s_full[s]);
                                 if (last_reader(s, j + 1)) mma_commit(&kv_empty[k.st]);
@@ -314,7 +341,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                             } else {
                                 mma_commit(&o_full[s]);
                             }
-                            if (last_reader(s, j)) mma_commit(&kv_empty[v.st]);
                         }
                     }
                 }
@@ -332,10 +358,9 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
     } else {
         // ============================================================ softmax, one warpgroup per stream
         reg_inc<216>();
-        const int s = warp >> 2, r = threadIdx.x & 127;
+        const int s = warp >> 2, lane_row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256 + s * D;
-        const int rt = r / a.G, rh = r % a.G;
         const float c = a.scale_log2;
         int ns_done = 0, no_done = 0, n_join = 0;
         bool ok = true;
@@ -344,13 +369,16 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             if (!(ok = wait(&item_full[ib], n / kItems, 3))) break;
             const int end = items[ib].end, g = items[ib].g, tok = items[ib].tok[s], ntok = items[ib].ntok[s],
                       nkeys = items[ib].nkeys[s], off = items[ib].off[s], slot = items[ib].slot;
-            const bool merge = !items[ib].shared && items[ib].nkeys[1] > 0;  // both streams hold parts of the same rows
+            const int one = items[ib].one;
+            const bool merge = !items[ib].shared && !one && items[ib].nkeys[1] > 0;  // both hold parts of the same rows
             __syncwarp();
             mbar_arrive_lane0(&item_empty[ib], lane);
             if (end) break;
             const int nt = tiles(nkeys);
             if (nt == 0) continue;
-            const bool warp_rows = (warp & 3) * 32 < ntok * a.G;  // some row of this warp is real
+            const int r = lane_row - (one && s ? kOneRow : 0);     // row of the stream's tile
+            const int rt = r / a.G, rh = r % a.G;
+            const bool warp_rows = r - lane >= 0 && r - lane < ntok * a.G;  // some row of this warp is real
             const int lim = min(nkeys - 1, off + rt);             // last key this row sees
             const int lim_all = min(nkeys - 1, off);              // ... that every row sees
             float m = -INFINITY, l = 0.f;
@@ -506,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             }
             const float inv = z > 0.f ? f / z : (z == 0.f ? 0.f : z), inv1 = merge && z > 0.f ? f1 / z : 0.f;  // NaN stays NaN
             const float lse = (mm + log2f(z)) * kLn2;
-            const int64_t prow = (int64_t)slot * a.B * a.hq + row;
+            const int64_t prow = (int64_t)(slot + (one ? s : 0)) * a.B * a.hq + row;
             if (warp_rows && real) {
                 if (a.decode) a.plse[prow] = lse;
                 else if (a.lse) a.lse[row] = lse;
@@ -573,9 +601,11 @@ cudaError_t launch(const Args &a, int64_t items, int32_t *next, cudaStream_t st)
     if (!have[0]) mk[0] = mk[1], mv[0] = mv[1];
     if (!ok) return cudaErrorInvalidValue;
     const size_t smem = Smem<D>::ALLOC;
-    const cudaError_t e = set_smem_once((const void *)fwd_tc_kernel<D>, smem);
+    cudaError_t e = set_smem_once((const void *)fwd_tc_kernel<D>, smem);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::min<int64_t>(items, sm_count());
+    if (!a.plan && items <= grid) next = nullptr;
+    else if (!a.plan && (e = cudaMemsetAsync(a.ds, 0, kWsHeader, st)) != cudaSuccess) return e;
     return launch_next(a.plan != nullptr, fwd_tc_kernel<D>, grid, kThreads, smem, st, mq, mq1, mk[0], mv[0], mk[1], mv[1],
                        a, next, wait_limit_ns());
 }

@@ -77,22 +77,30 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *cu, i
     }
 }
 
-// Joining the partials of a (sequence, head) row: weights e^{lse_i - max}, one block per
-// row, its warps taking every kJoinWarps-th slot (a warp reads a slot's d values as one
-// 512-byte line), their sums added in a fixed order.  Latency-bound: the slots of a row are
-// spread over as many warps as the reads need to be in flight together.
+// Joining the partials of a (sequence, head) row with weights e^{lse_i - max}.  W of the
+// block's 8 warps share a row, each taking every W-th slot (a warp reads a slot's d values
+// as one line), their sums added in a fixed order.  Latency-bound: with many slots per row
+// W = 8 keeps enough reads in flight (16 x 16 rows of 64 slots: 3 us of the 16.7 us step),
+// with few of them and many rows a warp per row is enough.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinMany = 8;  // slots from which a block takes one row
 
-template <typename T, int D>
+template <typename T, int D, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const __grid_constant__ Args a) {
     constexpr int E = D / 32;
     typedef typename std::conditional<E == 4, float4, float2>::type Vec;
     __shared__ float part[kJoinWarps][D + 1];
-    const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, warp = wid % W;
     const int64_t rows = (int64_t)a.B * a.hq;
+    const int row = blockIdx.x * (kJoinWarps / W) + wid / W;
     dependency_wait();
+    if (row >= rows) return;  // (W = 1 only)
     const int len = a.cap > 0 ? min(max(a.lens[row / a.hq], 0), a.cap) : 0;
-    const int n = a.pre_slots + (a.suf_sub > 0 ? (len + a.suf_sub - 1) / a.suf_sub : 0);
+    int n = a.pre_slots;
+    if (len > 0) {  // every item but the last is full; the last may lack its second stream's part
+        const int items = (len + a.suf_sub - 1) / a.suf_sub, rest = len - (items - 1) * a.suf_sub;
+        n += items * a.suf_per - (a.suf_per == 2 && rest <= first_half(rest));
+    }
     float m = a.off_by_one ? 0.f : -INFINITY;  // off-by-one: the added 1 is a logit of 0
     for (int i = lane; i < n; i += 32) m = fmaxf(m, a.plse[i * rows + row]);
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -101,7 +109,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const __grid_c
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-    for (int i = warp; i < n; i += kJoinWarps) {
+    for (int i = warp; i < n; i += W) {
         const float w = __expf(a.plse[i * rows + row] - mm);
         const Vec p = *reinterpret_cast<const Vec *>(a.po + (i * rows + row) * D + lane * E);
         z += w;
@@ -112,21 +120,38 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const __grid_c
             acc[3] += w * p.w;
         }
     }
+    T *o = static_cast<T *>(a.o) + (int64_t)row * D;
+    const float one = a.off_by_one ? __expf(-mm) : 0.f;
+    if constexpr (W == 1) {
+        z += one;
 #pragma unroll
-    for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
-    if (lane == 0) part[warp][D] = z;
-    __syncthreads();
-    if (threadIdx.x >= D) return;
-    float s = 0.f;
-    z = a.off_by_one ? __expf(-mm) : 0.f;
+        for (int e = 0; e < E; ++e) Elem<T>::store(o + lane * E + e, z == 0.f ? 0.f : acc[e] / z);
+        if (a.lse && lane == 0) a.lse[row] = mm + logf(z);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) {
-        s += part[i][threadIdx.x];
-        z += part[i][D];
+        for (int e = 0; e < E; ++e) part[wid][lane * E + e] = acc[e];
+        if (lane == 0) part[wid][D] = z;
+        __syncthreads();
+        if (threadIdx.x >= D) return;
+        float s = 0.f;
+        z = one;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            s += part[i][threadIdx.x];
+            z += part[i][D];
+        }
+        // no key at all: output 0, lse = log 0; a NaN stays one
+        Elem<T>::store(o + threadIdx.x, z == 0.f ? 0.f : s / z);
+        if (a.lse && threadIdx.x == 0) a.lse[row] = mm + logf(z);
     }
-    // no key at all: output 0, lse = log 0; a NaN stays one
-    Elem<T>::store(static_cast<T *>(a.o) + (int64_t)row * D + threadIdx.x, z == 0.f ? 0.f : s / z);
-    if (a.lse && threadIdx.x == 0) a.lse[row] = mm + logf(z);
+}
+
+template <typename T, int D> cudaError_t combine(const Args &a, cudaStream_t st) {
+    const bool behind = pre_items(a) + suf_items(a) > 0;  // else it is the call's first kernel
+    const int rows = a.B * a.hq;
+    if (a.pre_slots + a.suf_slots * a.suf_per >= kJoinMany)
+        return launch_next(behind, combine_kernel<T, D, kJoinWarps>, rows, kJoinWarps * 32, 0, st, a);
+    return launch_next(behind, combine_kernel<T, D, 1>, (rows + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, st, a);
 }
 
 }  // namespace
@@ -138,11 +163,8 @@ cudaError_t launch_plan(const int32_t *cu, int n_seq, int L, int tok, bool first
 }
 
 cudaError_t launch_combine(const Args &a, int d, bool bf16, cudaStream_t st) {
-    const int grid = a.B * a.hq;
-    const bool behind = pre_items(a) + suf_items(a) > 0;  // else it is the call's first kernel
-    auto go = [&](auto *kernel) { return launch_next(behind, kernel, grid, kJoinWarps * 32, 0, st, a); };
-    if (bf16) return d == 128 ? go(combine_kernel<__nv_bfloat16, 128>) : go(combine_kernel<__nv_bfloat16, 64>);
-    return d == 128 ? go(combine_kernel<float, 128>) : go(combine_kernel<float, 64>);
+    if (bf16) return d == 128 ? combine<__nv_bfloat16, 128>(a, st) : combine<__nv_bfloat16, 64>(a, st);
+    return d == 128 ? combine<float, 128>(a, st) : combine<float, 64>(a, st);
 }
 
 }  // namespace dense

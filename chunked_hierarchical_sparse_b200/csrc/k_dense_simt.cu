@@ -354,6 +354,7 @@ template <int D> constexpr size_t dkv_smem() { return sizeof(float) * (4 * kT * 
 template <typename T, int D> cudaError_t fwd(const Args &a, int64_t items, cudaStream_t st) {
     cudaError_t e = set_smem_once((const void *)fwd_simt_kernel<T, D>, fwd_smem<D>());
     if (e != cudaSuccess) return e;
+    if (!a.plan && (e = cudaMemsetAsync(a.ds, 0, kWsHeader, st)) != cudaSuccess) return e;
     return launch_next(a.plan != nullptr, fwd_simt_kernel<T, D>, (int)items, kThr, fwd_smem<D>(), st, a);
 }
 
