@@ -31,11 +31,10 @@ struct Args {
     // decode
     int cap;                     // tokens of a sequence's own cache
     const int32_t *lens;         // [B]
-    // The prefix is cut into pre_slots items of pre_sub keys, each own cache into suf_slots of
-    // suf_sub.  A prefix item's attention is one partial, in slot s; that of an own cache's
-    // item is suf_per partials (2: one per stream), in slots pre_slots + s suf_per + 0, 1.
+    // The prefix is cut into pre_slots slots of pre_sub keys, each own cache into suf_slots of
+    // suf_sub; an item takes one slot, whose attention is one partial.
     int pre_tiles, pre_sub, pre_slots;
-    int suf_sub, suf_slots, suf_per;
+    int suf_sub, suf_slots;
     int split;                   // tensor cores: a prefix item's two streams split its keys (its rows otherwise)
     // tensors: 0 = the prompt's (or the prefix's) keys and values, 1 = the own caches'
     const void *q, *k[2], *v[2];
@@ -54,16 +53,12 @@ struct Item {
     int plane;        // (batch, group) plane of k / v
     int key0, nkeys;  // first key and number of keys
     int off;          // row of token i sees key j (both relative) iff j <= off + i
-    int slot;         // decode: (first) partial slot
+    int slot;         // decode: partial slot
     int foreign;      // the last tile of 128 keys reaches beyond this sequence's own
 };
 
-__device__ __forceinline__ int own_len(const Args &a, int b) {
-    const int n = a.lens[b];
-    if (n >= 0 && n <= a.cap) return n;
-    report(a.ds, HSA_ERR_DEVICE_CHECK, kKDense, b, n);
-    return min(max(n, 0), a.cap);
-}
+// Tokens of sequence b's own (the join kernel reports a length outside [0, cap]).
+__device__ __forceinline__ int own_len(const Args &a, int b) { return min(max(a.lens[b], 0), a.cap); }
 
 __host__ __device__ __forceinline__ int pre_items(const Args &a) { return a.hkv * a.pre_tiles * a.pre_slots; }
 __host__ __device__ __forceinline__ int suf_items(const Args &a) { return a.hkv * a.B * a.suf_slots; }
@@ -101,22 +96,10 @@ __device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
     }
     it.off = kNoMask;
     it.foreign = 1;
-    // Prefix items (dear: many rows per key) come first, with one own-cache item (few rows
-    // per key) behind every two of them as far as they go, so that the ones' products run
-    // beside the others' reads and the small items are left for the end.
-    const int np = pre_items(a), mixed = 3 * min(np / 2, suf_items(a));
-    int before;  // prefix items among the first i
-    bool prefix;
-    if (i < mixed) {
-        before = i / 3 * 2 + (i % 3 != 0);
-        prefix = i % 3 != 1;
-    } else {
-        before = min(np, mixed / 3 * 2 + i - mixed);
-        prefix = before < np;
-    }
-    if (prefix) {
-        it.g = before % a.hkv;
-        const int r = before / a.hkv, tile = r % a.pre_tiles;
+    const int np = pre_items(a);
+    if (i < np) {
+        it.g = i % a.hkv;
+        const int r = i / a.hkv, tile = r % a.pre_tiles;
         it.slot = r / a.pre_tiles;
         it.tok0 = tile * a.tok;
         it.ntok = min(a.tok, a.B - it.tok0);
@@ -125,22 +108,19 @@ __device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
         it.key0 = it.slot * a.pre_sub;
         it.nkeys = min(a.pre_sub, a.L - it.key0);
     } else {
-        i -= before;
+        i -= np;
         it.g = i % a.hkv;
         const int r = i / a.hkv, s = r / a.B;
         it.tok0 = r % a.B;
         it.ntok = 1;
         it.src = 1;
         it.plane = it.tok0 * a.hkv + it.g;
-        it.slot = a.pre_slots + s * a.suf_per;
+        it.slot = a.pre_slots + s;
         it.key0 = s * a.suf_sub;
         it.nkeys = min(a.suf_sub, own_len(a, it.tok0) - it.key0);
     }
     return it.ntok > 0 && it.nkeys > 0;
 }
-
-// Keys of the first of two streams that split n, in whole tiles of 128.
-__host__ __device__ __forceinline__ int first_half(int n) { return (n + 255) / 256 * 128; }
 
 // ------------------------------------------------------------------ launches
 // A call's kernels run one behind the other on its stream.  Each but the first is
@@ -222,12 +202,14 @@ __device__ __forceinline__ bool get_key_item(const BwdArgs &b, int i, int keys, 
 
 // fp32, on the CUDA cores (tiles of kSimtRows rows and keys); clears the header likewise
 cudaError_t launch_fwd_simt(const Args &a, int d, int64_t items, cudaStream_t st);
-// bf16, on the tensor cores: a.tok is two row tiles (128 / G tokens each), but for a
+// bf16, on the tensor cores (decode: the prefix items): a.tok is two row tiles (128 / G tokens each), but for a
 // decode call whose batch fits one; `next`: an int32 of the header for the items dealt.
 // The header is cleared here where no kernel before it did (a.plan is null).
 cudaError_t launch_fwd_tc(const Args &a, int d, int64_t items, int32_t *next, cudaStream_t st);
 // a.tok = 128 / G, key tiles of 128; `next`: two zero int32
 cudaError_t launch_bwd_tc(const BwdArgs &b, int d, int64_t row_items, int64_t key_items, int32_t *next, cudaStream_t st);
+// bf16: the decode step's own caches; `first`: no kernel of the call ran before (clears the header)
+cudaError_t launch_cache(const Args &a, int d, bool first, cudaStream_t st);
 cudaError_t launch_combine(const Args &a, int d, bool bf16, cudaStream_t st);
 cudaError_t launch_delta(const BwdArgs &b, int d, bool bf16, cudaStream_t st);
 cudaError_t launch_bwd_simt(const BwdArgs &b, int d, int64_t row_items, int64_t key_items, cudaStream_t st);

@@ -123,7 +123,7 @@ hsa_status_t check_prompt_call(const hsa_prompt_shape_t *shape, const int32_t *c
 constexpr int kSms = 148;
 
 struct PrefixPlan {
-    int tok, split, pre_tiles, pre_sub, pre_slots, suf_sub, suf_slots, suf_per;
+    int tok, split, pre_tiles, pre_sub, pre_slots, suf_sub, suf_slots;
     size_t po, plse, bytes;  // workspace offsets
 };
 
@@ -149,20 +149,22 @@ int slot_keys(int64_t keys, int64_t jobs, int64_t want, int tile) {
 PrefixPlan plan_prefix(const hsa_prefix_shape_t &s) {
     PrefixPlan p{};
     const bool tc = s.dtype == HSA_BF16;
-    // a slot is worked on by two streams of 128 keys (tensor cores) or one of 64
-    const int G = s.h_q / s.h_kv, keys = tc ? 256 : kSimtRows, fit = (tc ? 128 : kSimtRows) / G;
-    // tensor cores: a batch beyond one row tile shares the keys between two row tiles,
-    // a smaller one (and every own cache) splits them between the two streams
+    const int G = s.h_q / s.h_kv, fit = (tc ? 128 : kSimtRows) / G;
+    // tensor cores: a batch beyond one row tile shares the keys between two row tiles, a
+    // smaller one splits them between the two streams
     p.split = tc && s.B <= fit;
     p.tok = tc && !p.split ? 2 * fit : fit;
     p.pre_tiles = (int)ceil_div(s.B, p.tok);
-    p.pre_sub = slot_keys(s.P, (int64_t)s.h_kv * p.pre_tiles, kSms, keys);
+    // the prefix: one item per SM (a second round of them costs more than it balances: 256 x 32K
+    // tokens 80 us, 96 with two rounds), of two tiles of 128 keys at least; on the CUDA cores
+    // about two blocks of 64-key tiles per SM
+    p.pre_sub = slot_keys(s.P, (int64_t)s.h_kv * p.pre_tiles, tc ? kSms : 2 * kSms, tc ? 256 : kSimtRows);
     p.pre_slots = p.pre_sub ? (int)ceil_div(s.P, p.pre_sub) : 0;
-    p.suf_sub = slot_keys(s.cap, (int64_t)s.h_kv * s.B, 2 * kSms, keys);
+    // the own caches: two blocks of four stages of 64 keys and more per SM
+    p.suf_sub = slot_keys(s.cap, (int64_t)s.h_kv * s.B, 2 * kSms, tc ? 256 : kSimtRows);
     p.suf_slots = p.suf_sub ? (int)ceil_div(s.cap, p.suf_sub) : 0;
-    p.suf_per = tc ? 2 : 1;
     Carver c{nullptr};
-    const size_t rows = (size_t)s.B * s.h_q * (p.pre_slots + p.suf_slots * p.suf_per);
+    const size_t rows = (size_t)s.B * s.h_q * (p.pre_slots + p.suf_slots);
     p.po = c.off;
     c.take<float>(rows * s.d);
     p.plse = c.off;
@@ -270,7 +272,7 @@ hsa_status_t hsa_prefix_decode(const hsa_prefix_shape_t *shape, const void *q, c
     a.cap = shape->cap; a.lens = lens;
     a.split = p.split;
     a.pre_tiles = p.pre_tiles; a.pre_sub = p.pre_sub; a.pre_slots = p.pre_slots;
-    a.suf_sub = p.suf_sub; a.suf_slots = p.suf_slots; a.suf_per = p.suf_per;
+    a.suf_sub = p.suf_sub; a.suf_slots = p.suf_slots;
     a.q = q;
     a.k[0] = k_prefix; a.v[0] = v_prefix; a.plane[0] = shape->prefix_stride;
     a.k[1] = k_cache; a.v[1] = v_cache; a.plane[1] = (int64_t)shape->cap * shape->d;
@@ -278,13 +280,19 @@ hsa_status_t hsa_prefix_decode(const hsa_prefix_shape_t *shape, const void *q, c
     a.po = reinterpret_cast<float *>(static_cast<char *>(ws) + p.po);
     a.plse = reinterpret_cast<float *>(static_cast<char *>(ws) + p.plse);
     a.ds = static_cast<DevStatus *>(ws);
-    const int64_t items = (int64_t)pre_items(a) + suf_items(a);
-    TimedLaunch tl(HSA_K_PREFIX, items > 0 ? 2 : 1, st);
-    if (items > 0)
-        e = bf16 ? launch_fwd_tc(a, shape->d, items, word(ws, kWordNext), st)
-                 : launch_fwd_simt(a, shape->d, items, st);
-    else
-        e = cudaMemsetAsync(ws, 0, kWsHeader, st);
+    const int np = pre_items(a), ns = suf_items(a);
+    TimedLaunch tl(HSA_K_PREFIX, 1 + (bf16 ? (np > 0) + (ns > 0) : np + ns > 0), st);
+    if (bf16) {
+        if (np > 0) {
+            Args pre = a;
+            pre.suf_slots = 0;
+            e = launch_fwd_tc(pre, shape->d, np, word(ws, kWordNext), st);
+        }
+        if (e == cudaSuccess && ns > 0) e = launch_cache(a, shape->d, np == 0, st);
+    } else if (np + ns > 0) {
+        e = launch_fwd_simt(a, shape->d, (int64_t)np + ns, st);
+    }
+    if (np + ns == 0) e = cudaMemsetAsync(ws, 0, kWsHeader, st);
     if (e == cudaSuccess) e = launch_combine(a, shape->d, bf16, st);
     return cuda_status(e);
 }

@@ -1,5 +1,5 @@
 // k_dense_fwd_tc.cu -- dense attention on the tensor cores (bf16): the prompt pass
-// and the partial passes of the shared-prefix decode step.
+// and the prefix part of the shared-prefix decode step.
 //
 // Mathematics.  For a tile of 128 (token, head) rows, keys in tiles of 128:
 // S = Q K^T, p = 2^(s c - m), l += sum p, O += P V with c = log2(e)/sqrt(d), one
@@ -16,10 +16,11 @@
 // P.V(j), S(j+1), so S may overwrite the P that the product before it reads, and
 // a finished S(j+1) means that O holds tiles 0..j.
 // - Prompt pass: the streams are neighbouring row tiles and share the K and V tiles.
-// - Decode, more rows than one tile (prefix): likewise.
-// - Decode otherwise: both streams hold the same rows and take half of the keys each.
-// Warp 8 deals the items (dynamically, dearest first) and loads by TMA, warp 9
-// issues the MMAs.
+// - Decode, more rows than one tile: likewise.
+// - Decode, one row tile: both streams hold the same rows and take half of the keys
+//   each; their results are joined in the epilogue.
+// Warp 8 deals the items (dynamically, dearest first) and loads K and V by TMA, warp 9
+// issues the MMAs, warp 10 clears foreign rows, warp 11 loads Q.
 #include <algorithm>
 #include <atomic>
 
@@ -34,8 +35,6 @@ constexpr int kThreads = 384;
 constexpr int kKeys = 128;        // keys per tile
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpClear = 10, kWarpQ = 11;
 constexpr int kItems = 3;         // item ring
-constexpr int kOneRow = 32;       // first row of stream 1 of a one-token item (at most 16 rows): the streams'
-                                  // softmaxes are then warps of different schedulers
 constexpr float kSlack = 8.f;     // log2 of how far a tile may exceed m before it moves
 
 template <int D> struct Smem {
@@ -53,7 +52,7 @@ template <int D> struct Smem {
 static_assert(Smem<128>::ALLOC <= 232448 && Smem<64>::ALLOC <= 232448, "shared memory of a CTA");
 
 struct TcItem {
-    int end, src, plane, g, one, shared, foreign, slot;  // one: load the single token's rows only
+    int end, plane, g, shared, foreign, slot;
     int tok[2], ntok[2], key0[2], nkeys[2], off[2];
 };
 static_assert(kItems * sizeof(TcItem) <= 256, "item ring");
@@ -63,8 +62,8 @@ __device__ __forceinline__ bool get_tc_item(const Args &a, int i, TcItem &t) {
     Item it;
     const bool some = get_item(a, i, it);
     const int tt = a.decode ? 128 / a.G : a.tok / 2;  // tokens of one stream's tile (shared keys)
-    t.end = 0; t.src = it.src; t.plane = it.plane; t.g = it.g; t.one = 0;
-    t.shared = !a.decode || (it.src == 0 && !a.split);
+    t.end = 0; t.plane = it.plane; t.g = it.g;
+    t.shared = !a.decode || !a.split;
     t.foreign = it.foreign; t.slot = it.slot;
     if (t.shared) {
 #pragma unroll
@@ -76,8 +75,7 @@ __device__ __forceinline__ bool get_tc_item(const Args &a, int i, TcItem &t) {
             t.nkeys[s] = t.ntok[s] <= 0 ? 0 : (it.off == kNoMask ? it.nkeys : min(it.nkeys, t.off[s] + t.ntok[s]));
         }
     } else {  // half of the keys each, in whole tiles
-        const int half = first_half(it.nkeys);
-        t.one = it.src;  // its partials are not joined here: stream 1's rows are on other lanes
+        const int half = (it.nkeys + 2 * kKeys - 1) / (2 * kKeys) * kKeys;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             t.tok[s] = it.tok0;
@@ -111,9 +109,8 @@ __device__ __forceinline__ void rescale16(uint32_t t, float f) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
-    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
-    const __grid_constant__ CUtensorMap tm_k0, const __grid_constant__ CUtensorMap tm_v0,
-    const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_v1,
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+    const __grid_constant__ CUtensorMap tm_v,
     const __grid_constant__ Args a, int32_t *next, uint64_t wait_ns) {
     using L = Smem<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -148,18 +145,18 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
         tmem_relinquish();
     }
     if (warp == kWarpLoad && lane == 0) {
-        prefetch_tmap(&tm_q); prefetch_tmap(&tm_k0); prefetch_tmap(&tm_v0);
+        prefetch_tmap(&tm_q); prefetch_tmap(&tm_k); prefetch_tmap(&tm_v);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
     dependency_wait();
-    dependents_may_start();
     // A call of at most one item per block needs no counter and clears its header here: the
     // other blocks report nothing but waits that ran out, seconds later.
     if (!next && blockIdx.x == 0 && threadIdx.x == 0) *a.ds = DevStatus{};
     if (!next) __syncthreads();
+    dependents_may_start();
     auto wait = [&](uint64_t *b, uint32_t par, int role) { return warp_wait(b, par & 1, wait_ns, abort_flag, a.ds, role); };
     auto tiles = [](int keys) { return (keys + kKeys - 1) / kKeys; };
 
@@ -191,7 +188,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                 }
                 __syncwarp();
                 if (t.end) break;
-                const CUtensorMap *mk = t.src ? &tm_k1 : &tm_k0, *mv = t.src ? &tm_v1 : &tm_v0;
                 auto load_kv = [&](const CUtensorMap *m, int key) -> bool {
                     const int st = kv % L::ST;
                     if (kv >= L::ST && !wait(&kv_empty[st], kv / L::ST - 1, 1)) return false;
@@ -205,23 +201,23 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                     return true;
                 };
                 const int n0 = tiles(t.nkeys[0]), n1 = tiles(t.nkeys[1]);
-                ok = load_kv(mk, t.key0[0]);
-                if (ok && !t.shared && n1) ok = load_kv(mk, t.key0[1]);
+                ok = load_kv(&tm_k, t.key0[0]);
+                if (ok && !t.shared && n1) ok = load_kv(&tm_k, t.key0[1]);
                 idx = next_item();
                 look_up(ahead);
                 if (t.shared) {
                     const int nn = max(n0, n1);
                     for (int j = 0; ok && j < nn; ++j) {
-                        ok = load_kv(mv, t.key0[0] + j * kKeys);
-                        if (ok && j + 1 < nn) ok = load_kv(mk, t.key0[0] + (j + 1) * kKeys);
+                        ok = load_kv(&tm_v, t.key0[0] + j * kKeys);
+                        if (ok && j + 1 < nn) ok = load_kv(&tm_k, t.key0[0] + (j + 1) * kKeys);
                     }
                 } else {
                     for (int j = 0; ok && j < n0; ++j) {
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
                             const int ns = s ? n1 : n0;
-                            if (ok && j < ns) ok = load_kv(mv, t.key0[s] + j * kKeys);
-                            if (ok && j + 1 < ns) ok = load_kv(mk, t.key0[s] + (j + 1) * kKeys);
+                            if (ok && j < ns) ok = load_kv(&tm_v, t.key0[s] + j * kKeys);
+                            if (ok && j + 1 < ns) ok = load_kv(&tm_k, t.key0[s] + (j + 1) * kKeys);
                         }
                     }
                 }
@@ -247,12 +243,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                     if (!ok || t.nkeys[s] == 0) continue;
                     if (nq[s] > 0 && !(ok = wait(&q_empty[s], nq[s] - 1, 5))) break;
                     if (lane == 0) {
-                        const int rows = t.one ? a.G : a.G * (128 / a.G);
-                        mbar_arrive_expect_tx(&q_full[s], L::NH * rows * 128);
+                        mbar_arrive_expect_tx(&q_full[s], L::NH * a.G * (128 / a.G) * 128);
 #pragma unroll
                         for (int h = 0; h < L::NH; ++h)
-                            tma_load_3d(sm + L::OFF_Q + s * L::TILE + h * 16384 + (t.one && s ? kOneRow * 128 : 0),
-                                        t.one ? &tm_q1 : &tm_q, h * 64, t.g * a.G, t.tok[s], &q_full[s]);
+                            tma_load_3d(sm + L::OFF_Q + s * L::TILE + h * 16384, &tm_q, h * 64, t.g * a.G, t.tok[s], &q_full[s]);
                     }
                     ++nq[s];
                 }
@@ -358,9 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
     } else {
         // ============================================================ softmax, one warpgroup per stream
         reg_inc<216>();
-        const int s = warp >> 2, lane_row = threadIdx.x & 127;
+        const int s = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256 + s * D;
+        const int rt = r / a.G, rh = r % a.G;
         const float c = a.scale_log2;
         int ns_done = 0, no_done = 0, n_join = 0;
         bool ok = true;
@@ -369,16 +364,13 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             if (!(ok = wait(&item_full[ib], n / kItems, 3))) break;
             const int end = items[ib].end, g = items[ib].g, tok = items[ib].tok[s], ntok = items[ib].ntok[s],
                       nkeys = items[ib].nkeys[s], off = items[ib].off[s], slot = items[ib].slot;
-            const int one = items[ib].one;
-            const bool merge = !items[ib].shared && !one && items[ib].nkeys[1] > 0;  // both hold parts of the same rows
+            const bool merge = !items[ib].shared && items[ib].nkeys[1] > 0;  // both streams hold parts of the same rows
             __syncwarp();
             mbar_arrive_lane0(&item_empty[ib], lane);
             if (end) break;
             const int nt = tiles(nkeys);
             if (nt == 0) continue;
-            const int r = lane_row - (one && s ? kOneRow : 0);     // row of the stream's tile
-            const int rt = r / a.G, rh = r % a.G;
-            const bool warp_rows = r - lane >= 0 && r - lane < ntok * a.G;  // some row of this warp is real
+            const bool warp_rows = r - lane < ntok * a.G;         // some row of this warp is real
             const int lim = min(nkeys - 1, off + rt);             // last key this row sees
             const int lim_all = min(nkeys - 1, off);              // ... that every row sees
             float m = -INFINITY, l = 0.f;
@@ -534,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             }
             const float inv = z > 0.f ? f / z : (z == 0.f ? 0.f : z), inv1 = merge && z > 0.f ? f1 / z : 0.f;  // NaN stays NaN
             const float lse = (mm + log2f(z)) * kLn2;
-            const int64_t prow = (int64_t)(slot + (one ? s : 0)) * a.B * a.hq + row;
+            const int64_t prow = (int64_t)slot * a.B * a.hq + row;
             if (warp_rows && real) {
                 if (a.decode) a.plse[prow] = lse;
                 else if (a.lse) a.lse[row] = lse;
@@ -585,29 +577,20 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
 
 template <int D>
 cudaError_t launch(const Args &a, int64_t items, int32_t *next, cudaStream_t st) {
-    CUtensorMap mq, mq1, mk[2], mv[2];
-    const uint64_t rows = (uint64_t)a.B * (a.decode ? 1 : a.L), tt = 128 / a.G;
-    bool ok = make_map3(&mq, a.q, D, a.hq, D, rows, (uint64_t)a.hq * D, a.G, (uint32_t)tt);
-    const bool have[2] = {a.L > 0, a.decode && a.cap > 0};
-    for (int i = 0; ok && i < 2; ++i) {
-        if (!have[i]) continue;
-        const uint64_t n = i ? a.cap : a.L, planes = a.decode && !i ? a.hkv : (uint64_t)a.B * a.hkv;
-        ok = make_map3(&mk[i], a.k[i], D, n, D, planes, a.plane[i], kKeys, 1) &&
-             make_map3(&mv[i], a.v[i], D, n, D, planes, a.plane[i], kKeys, 1);
-    }
-    // maps that no item reads through
-    if (have[1]) ok = ok && make_map3(&mq1, a.q, D, a.hq, D, rows, (uint64_t)a.hq * D, a.G, 1);
-    else mq1 = mq, mk[1] = mk[0], mv[1] = mv[0];
-    if (!have[0]) mk[0] = mk[1], mv[0] = mv[1];
-    if (!ok) return cudaErrorInvalidValue;
+    CUtensorMap mq, mk, mv;
+    const uint64_t rows = (uint64_t)a.B * (a.decode ? 1 : a.L), planes = (uint64_t)a.hkv * (a.decode ? 1 : a.B);
+    if (!make_map3(&mq, a.q, D, a.hq, D, rows, (uint64_t)a.hq * D, a.G, 128 / a.G) ||
+        !make_map3(&mk, a.k[0], D, a.L, D, planes, a.plane[0], kKeys, 1) ||
+        !make_map3(&mv, a.v[0], D, a.L, D, planes, a.plane[0], kKeys, 1))
+        return cudaErrorInvalidValue;
     const size_t smem = Smem<D>::ALLOC;
     cudaError_t e = set_smem_once((const void *)fwd_tc_kernel<D>, smem);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::min<int64_t>(items, sm_count());
     if (!a.plan && items <= grid) next = nullptr;
     else if (!a.plan && (e = cudaMemsetAsync(a.ds, 0, kWsHeader, st)) != cudaSuccess) return e;
-    return launch_next(a.plan != nullptr, fwd_tc_kernel<D>, grid, kThreads, smem, st, mq, mq1, mk[0], mv[0], mk[1], mv[1],
-                       a, next, wait_limit_ns());
+    return launch_next(a.plan != nullptr, fwd_tc_kernel<D>, grid, kThreads, smem, st, mq, mk, mv, a, next,
+                       wait_limit_ns());
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,

@@ -95,12 +95,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const __grid_c
     const int row = blockIdx.x * (kJoinWarps / W) + wid / W;
     dependency_wait();
     if (row >= rows) return;  // (W = 1 only)
-    const int len = a.cap > 0 ? min(max(a.lens[row / a.hq], 0), a.cap) : 0;
-    int n = a.pre_slots;
-    if (len > 0) {  // every item but the last is full; the last may lack its second stream's part
-        const int items = (len + a.suf_sub - 1) / a.suf_sub, rest = len - (items - 1) * a.suf_sub;
-        n += items * a.suf_per - (a.suf_per == 2 && rest <= first_half(rest));
-    }
+    const int len = a.cap > 0 ? own_len(a, row / a.hq) : 0;
+    if (a.cap > 0 && row % a.hq == 0 && warp == 0 && lane == 0 && a.lens[row / a.hq] != len)
+        report(a.ds, HSA_ERR_DEVICE_CHECK, kKDense, row / a.hq, a.lens[row / a.hq]);
+    const int n = a.pre_slots + (len > 0 ? (len + a.suf_sub - 1) / a.suf_sub : 0);
     float m = a.off_by_one ? 0.f : -INFINITY;  // off-by-one: the added 1 is a logit of 0
     for (int i = lane; i < n; i += 32) m = fmaxf(m, a.plse[i * rows + row]);
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -149,7 +147,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) combine_kernel(const __grid_c
 template <typename T, int D> cudaError_t combine(const Args &a, cudaStream_t st) {
     const bool behind = pre_items(a) + suf_items(a) > 0;  // else it is the call's first kernel
     const int rows = a.B * a.hq;
-    if (a.pre_slots + a.suf_slots * a.suf_per >= kJoinMany)
+    if (a.pre_slots + a.suf_slots >= kJoinMany)
         return launch_next(behind, combine_kernel<T, D, kJoinWarps>, rows, kJoinWarps * 32, 0, st, a);
     return launch_next(behind, combine_kernel<T, D, 1>, (rows + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, st, a);
 }
