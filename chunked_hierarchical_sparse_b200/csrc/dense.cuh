@@ -25,9 +25,9 @@ struct Args {
     int off_by_one;
     float scale, scale_log2;     // 1 / sqrt(d), and that times log2(e)
     // prompt pass
-    const int4 *plan;            // packed: {first token, tokens, tile, 0} per tile, dearest first (else null)
-    const int32_t *plan_n;       //         entries in `plan`
-    int tiles;                   // not packed: row tiles per batch row
+    const int4 *plan;            // packed: {sequence's first token, its length, item's first token, split},
+    const int32_t *plan_n;       //         dearest first (else null), and the entries in it
+    int tiles;                   // not packed: items per batch row
     // decode
     int cap;                     // tokens of a sequence's own cache
     const int32_t *lens;         // [B]
@@ -35,7 +35,8 @@ struct Args {
     // suf_sub; an item takes one slot, whose attention is one partial.
     int pre_tiles, pre_sub, pre_slots;
     int suf_sub, suf_slots;
-    int split;                   // tensor cores: a prefix item's two streams split its keys (its rows otherwise)
+    int split;                   // tensor cores, decode or not packed: an item's two streams have the same rows
+                                 // and split the keys (else they have a tile of rows each)
     // tensors: 0 = the prompt's (or the prefix's) keys and values, 1 = the own caches'
     const void *q, *k[2], *v[2];
     int64_t plane[2];            // elements between two (batch, group) planes of k[i] / v[i]
@@ -54,6 +55,7 @@ struct Item {
     int key0, nkeys;  // first key and number of keys
     int off;          // row of token i sees key j (both relative) iff j <= off + i
     int slot;         // decode: partial slot
+    int split;        // the streams split the keys
     int foreign;      // the last tile of 128 keys reaches beyond this sequence's own
 };
 
@@ -71,20 +73,20 @@ __device__ __forceinline__ int item_count(const Args &a) {
 // Item i of the call, dearest first; false when it has no rows or no keys.
 __device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
     if (!a.decode) {
-        int start, len, tile, b;
+        int start, len, t, b, tok = a.tok;
         if (a.plan) {
             const int4 p = a.plan[i / a.hkv];
             it.g = i % a.hkv;
-            b = 0; start = p.x; len = p.y; tile = p.z;
+            b = 0; start = p.x; len = p.y; t = p.z; it.split = p.w;
         } else {
             const int bh = i % (a.B * a.hkv);
             b = bh / a.hkv;
             it.g = bh % a.hkv;
-            start = 0; len = a.L; tile = a.tiles - 1 - i / (a.B * a.hkv);
+            start = 0; len = a.L; t = (a.tiles - 1 - i / (a.B * a.hkv)) * tok; it.split = a.split;
         }
-        const int t = tile * a.tok;
+        if (a.plan && it.split) tok /= 2;
         it.tok0 = b * a.L + start + t;
-        it.ntok = min(a.tok, len - t);
+        it.ntok = min(tok, len - t);
         it.src = 0;
         it.plane = b * a.hkv + it.g;
         it.key0 = start;
@@ -96,6 +98,7 @@ __device__ __forceinline__ bool get_item(const Args &a, int i, Item &it) {
     }
     it.off = kNoMask;
     it.foreign = 1;
+    it.split = a.split;
     const int np = pre_items(a);
     if (i < np) {
         it.g = i % a.hkv;
@@ -148,20 +151,49 @@ cudaError_t launch_next(bool behind_kernel, void (*kernel)(P...), int grid, int 
 }
 
 // ------------------------------------------------------------------ launchers
-// Packed prompts: the tiles of `tok` tokens of every sequence, dearest first
-// (first_dear: the cost of a sequence's tiles falls with their index -- the tiles
-// of keys of the backward -- instead of rising).  A cu_seqlens that does not rise
-// inside [0, L] is reported and gives no tiles.
-// The first of a call's launches (`clear`) also zeroes the workspace header.
-cudaError_t launch_plan(const int32_t *cu, int n_seq, int L, int tok, bool first_dear, int4 *plan, int32_t *plan_n,
-                        DevStatus *ds, bool clear, cudaStream_t st);
+// Work lists, made on the device from the sequences' bounds: the items of a job, dearest
+// first.  A cu_seqlens that does not rise inside [0, L] is reported and gives no items.
+enum PlanKind {
+    kRows,       // tiles of `tok` tokens
+    kRowsSplit,  // the same; sequences too long for their tiles to be one SM's share of the work are
+                 // cut into tiles of half as many tokens, whose two streams split the keys
+    kKeys,       // tiles of `tok` keys
+    kKeysSplit   // tiles of 128 keys; where more rows see a tile than key_limit allows, in pieces
+};
+constexpr int kPlanSms = 148;
+struct PlanJob {
+    int kind;
+    const int32_t *cu;  // null: n_seq sequences of L tokens each
+    int n_seq, L, tok, G, hkv;
+    int4 *plan, *piece;  // kRows*: {first token, length, item's first token, split}; kKeys*: {.., .., tile, piece}
+    int32_t *n;          // piece: {first row tile, end, partial slot of group 0 or -1, 0}
+    int4 *cut;           // kKeysSplit: {first token, length, tile, slot | pieces << 16} of every cut tile
+    int32_t *n_cut;
+};
+// Row tiles of a piece: half an SM's share of `work` steps, but worth its partial (8 steps).
+// A cut tile has fewer than 2 rows / limit pieces, so all cut tiles together have fewer
+// than 4 kPlanSms: the number of partial slots is bounded whatever the lengths are.
+__host__ __device__ __forceinline__ int key_limit(unsigned long long work) {
+    const unsigned long long l = (work + 2 * kPlanSms - 1) / (2 * kPlanSms);
+    return l < 8 ? 8 : l > 0x3fffffff ? 0x3fffffff : (int)l;
+}
+constexpr int kMaxPieces = 4 * kPlanSms;
+// words of the workspace header behind the status word
+constexpr int kHeaderWords = (int)(kWsHeader / 4), kWordPlanN = 8, kWordKPlanN = 9, kWordCutN = 10,
+              kWordNext = 32;
+__device__ __forceinline__ bool header_word_of_plan(int i) { return i >= kWordPlanN && i <= kWordCutN; }
+// The first of a call's launches: also zeroes the rest of the header.
+cudaError_t launch_plan(const PlanJob &job0, const PlanJob *job1, DevStatus *ds, cudaStream_t st);
 inline int64_t plan_cap(int L, int n_seq, int tok) { return (int64_t)L / tok + n_seq; }
 
 struct BwdArgs {
     Args a;                      // a.plan: the row tiles; a.q, a.k, a.v as in the forward
-    const int4 *kplan;           // packed: the key tiles
+    const int4 *kplan, *kpiece;  // the key tiles (PlanJob; else null: ktiles per batch row, uncut)
     const int32_t *kplan_n;
-    int ktiles;                  // not packed: key tiles per batch row
+    int ktiles;
+    const int4 *cut;             // the tiles whose rows are cut into pieces (PlanJob)
+    const int32_t *n_cut;
+    float *part;                 // partials of cut tiles [slot][dv, dk][128][d]
     const void *o, *dO;
     const float *lse;
     float *delta;                // [B*L, h_q]  dO . o
@@ -174,6 +206,8 @@ struct KeyItem {
     int start, len;     // the sequence inside its batch row
     int n0, nkeys;      // first key (of the sequence) and keys
     int g, plane;
+    int j0, j1;         // tensor cores: row tiles (of 128 / G tokens) to walk
+    int slot;           // partial slot, or -1: the only piece
 };
 
 __device__ __forceinline__ int key_item_count(const BwdArgs &b) {
@@ -186,7 +220,7 @@ __device__ __forceinline__ bool get_key_item(const BwdArgs &b, int i, int keys, 
     if (b.kplan) {
         const int4 p = b.kplan[i / b.a.hkv];
         it.g = i % b.a.hkv;
-        row = 0; it.start = p.x; it.len = p.y; tile = p.z;
+        row = p.x / b.a.L; it.start = p.x % b.a.L; it.len = p.y; tile = p.z;
     } else {
         const int bh = i % (b.a.B * b.a.hkv);
         row = bh / b.a.hkv;
@@ -197,6 +231,17 @@ __device__ __forceinline__ bool get_key_item(const BwdArgs &b, int i, int keys, 
     it.n0 = tile * keys;
     it.nkeys = min(keys, it.len - it.n0);
     it.plane = row * b.a.hkv + it.g;
+    if (b.kpiece) {
+        const int4 c = b.kpiece[i / b.a.hkv];
+        it.j0 = c.x;
+        it.j1 = c.y;
+        it.slot = c.z < 0 ? -1 : c.z + it.g;
+    } else {
+        const int tt = 128 / b.a.G;
+        it.j0 = it.n0 / tt;
+        it.j1 = (it.len + tt - 1) / tt;
+        it.slot = -1;
+    }
     return it.nkeys > 0;
 }
 
@@ -211,6 +256,7 @@ cudaError_t launch_bwd_tc(const BwdArgs &b, int d, int64_t row_items, int64_t ke
 // bf16: the decode step's own caches; `first`: no kernel of the call ran before (clears the header)
 cudaError_t launch_cache(const Args &a, int d, bool first, cudaStream_t st);
 cudaError_t launch_combine(const Args &a, int d, bool bf16, cudaStream_t st);
+cudaError_t launch_add_pieces(const BwdArgs &b, int d, cudaStream_t st);
 cudaError_t launch_delta(const BwdArgs &b, int d, bool bf16, cudaStream_t st);
 cudaError_t launch_bwd_simt(const BwdArgs &b, int d, int64_t row_items, int64_t key_items, cudaStream_t st);
 

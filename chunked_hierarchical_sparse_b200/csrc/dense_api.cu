@@ -33,8 +33,6 @@ struct Carver {
     }
 };
 
-// words of the workspace header behind the status word (all cleared by every call)
-constexpr int kWordPlanN = 8, kWordKPlanN = 9, kWordNext = 32;
 int32_t *word(void *ws, int i) { return static_cast<int32_t *>(ws) + i; }
 
 hsa_status_t check_heads(int h_q, int h_kv, int d, int off_by_one, int dtype) {
@@ -58,28 +56,63 @@ hsa_status_t check_prompt(const hsa_prompt_shape_t *s) {
 }
 
 struct PromptWs {
-    int4 *plan, *kplan;
-    float *delta;
+    int4 *plan, *kplan, *kpiece, *cut;
+    float *delta, *part;
     size_t bytes;
 };
 
-// tokens of a row item: 64 rows on the CUDA cores (fp32), two tiles of 128 rows on the
-// tensor cores (bf16)
-int row_tile(const hsa_prompt_shape_t &s) {
-    const int G = s.h_q / s.h_kv;
-    return s.dtype == HSA_BF16 ? 2 * (128 / G) : kSimtRows / G;
+bool tensor_cores(const hsa_prompt_shape_t &s) { return s.dtype == HSA_BF16; }
+int group(const hsa_prompt_shape_t &s) { return s.h_q / s.h_kv; }
+int64_t row_items(const hsa_prompt_shape_t &s, int tok) {
+    return s.n_seq > 0 ? plan_cap(s.L, s.n_seq, tok) * s.h_kv : (int64_t)s.B * s.h_kv * ceil_div(s.L, tok);
 }
-// the backward's: one tile of rows, and its tiles of keys
-int bwd_row_tile(const hsa_prompt_shape_t &s) { return (s.dtype == HSA_BF16 ? 128 : kSimtRows) / (s.h_q / s.h_kv); }
-int bwd_key_tile(const hsa_prompt_shape_t &s) { return s.dtype == HSA_BF16 ? 128 : kSimtRows; }
+
+// Forward, tensor cores, not packed: two row tiles per item where that fills the GPU, else
+// one, whose streams split the keys (4K tokens, 16 heads in 2 groups: NN us, MM without).
+bool fwd_split(const hsa_prompt_shape_t &s) {
+    return tensor_cores(s) && s.n_seq == 0 && row_items(s, 2 * (128 / group(s))) <= kPlanSms;
+}
+// tokens of a row item: 64 rows on the CUDA cores (fp32), 128-row tiles on the tensor cores
+int fwd_tok(const hsa_prompt_shape_t &s) {
+    return tensor_cores(s) ? (fwd_split(s) ? 1 : 2) * (128 / group(s)) : kSimtRows / group(s);
+}
+int bwd_tok(const hsa_prompt_shape_t &s) { return (tensor_cores(s) ? 128 : kSimtRows) / group(s); }
+int key_tile(const hsa_prompt_shape_t &s) { return tensor_cores(s) ? 128 : kSimtRows; }
+
+// Backward, tensor cores: steps of the key pass (not packed: exactly; packed: at most) and
+// whether some key tile's rows are cut into pieces.
+uint64_t key_steps(const hsa_prompt_shape_t &s) {
+    const int tt = 128 / group(s);
+    const int64_t n = ceil_div(s.L, 128), rows = ceil_div(s.L, tt);
+    uint64_t w = 0;
+    for (int64_t i = 0; i < n; ++i) w += rows - i * 128 / tt;
+    return w * s.h_kv * s.B;
+}
+bool key_pieces(const hsa_prompt_shape_t &s) {
+    if (!tensor_cores(s)) return false;
+    return s.n_seq > 0 || ceil_div(s.L, 128 / group(s)) > key_limit(key_steps(s));
+}
 
 PromptWs carve_prompt(const hsa_prompt_shape_t &s, void *ws, bool bwd) {
     Carver c{static_cast<char *>(ws)};
     PromptWs w{};
-    if (s.n_seq > 0) w.plan = c.take<int4>(plan_cap(s.L, s.n_seq, bwd ? bwd_row_tile(s) : row_tile(s)));
+    // a packed forward may cut every sequence into half-size items
+    if (s.n_seq > 0)
+        w.plan = c.take<int4>(plan_cap(s.L, s.n_seq, bwd ? bwd_tok(s) : tensor_cores(s) ? 128 / group(s) : fwd_tok(s)));
     if (bwd) {
-        if (s.n_seq > 0) w.kplan = c.take<int4>(plan_cap(s.L, s.n_seq, bwd_key_tile(s)));
         w.delta = c.take<float>((size_t)s.B * s.L * s.h_q);
+        const bool pieces = key_pieces(s);
+        if (pieces || s.n_seq > 0) {
+            const int64_t n = s.n_seq > 0 ? plan_cap(s.L, s.n_seq, key_tile(s)) : (int64_t)s.B * ceil_div(s.L, key_tile(s));
+            w.kplan = c.take<int4>(n + (pieces ? kMaxPieces : 0));
+            if (pieces) {
+                w.kpiece = c.take<int4>(n + kMaxPieces);
+                w.cut = c.take<int4>(std::min<int64_t>(n, kMaxPieces));
+                // pieces have more than 4 row tiles each, which bounds their number for short rows
+                const int64_t most = n * s.h_kv * (1 + ceil_div(s.L, 128 / group(s)) / 4);
+                w.part = c.take<float>((size_t)std::min<int64_t>(kMaxPieces, most) * 2 * 128 * s.d);
+            }
+        }
     }
     w.bytes = c.off;
     return w;
@@ -88,7 +121,7 @@ PromptWs carve_prompt(const hsa_prompt_shape_t &s, void *ws, bool bwd) {
 Args prompt_args(const hsa_prompt_shape_t &s, const void *q, const void *k, const void *v, void *ws, const PromptWs &w,
                  int tok) {
     Args a{};
-    a.B = s.B; a.L = s.L; a.hq = s.h_q; a.hkv = s.h_kv; a.G = s.h_q / s.h_kv;
+    a.B = s.B; a.L = s.L; a.hq = s.h_q; a.hkv = s.h_kv; a.G = group(s);
     a.tok = tok;
     a.off_by_one = s.off_by_one;
     a.scale = 1.0f / sqrtf((float)s.d);
@@ -102,8 +135,14 @@ Args prompt_args(const hsa_prompt_shape_t &s, const void *q, const void *k, cons
     return a;
 }
 
-int64_t max_items(const hsa_prompt_shape_t &s, int tok) {
-    return s.n_seq > 0 ? plan_cap(s.L, s.n_seq, tok) * s.h_kv : (int64_t)s.B * s.h_kv * ceil_div(s.L, tok);
+PlanJob plan_job(const hsa_prompt_shape_t &s, PlanKind kind, const int32_t *cu, int tok, int4 *plan, int4 *piece, int32_t *n) {
+    PlanJob j{};
+    j.kind = kind;
+    j.cu = cu;
+    j.n_seq = cu ? s.n_seq : s.B;
+    j.L = s.L; j.tok = tok; j.G = group(s); j.hkv = s.h_kv;
+    j.plan = plan; j.piece = piece; j.n = n;
+    return j;
 }
 
 // checks shared by the two directions; *empty: nothing to read or write
@@ -155,13 +194,26 @@ PrefixPlan plan_prefix(const hsa_prefix_shape_t &s) {
     p.split = tc && s.B <= fit;
     p.tok = tc && !p.split ? 2 * fit : fit;
     p.pre_tiles = (int)ceil_div(s.B, p.tok);
-    // the prefix: one item per SM (a second round of them costs more than it balances: 256 x 32K
-    // tokens 80 us, 96 with two rounds), of two tiles of 128 keys at least; on the CUDA cores
-    // about two blocks of 64-key tiles per SM
-    p.pre_sub = slot_keys(s.P, (int64_t)s.h_kv * p.pre_tiles, tc ? kSms : 2 * kSms, tc ? 256 : kSimtRows);
+    if (tc) {
+        // The prefix: one item per SM, of two tiles of 128 keys at least (a second round of
+        // items costs more than it balances: 256 x 32K tokens 80 us, 96 with two rounds).  Where
+        // it keeps every SM for long (8 steps of 256 x 128 and more), it leaves to the own caches,
+        // which are bound by HBM, as many SMs as let them finish beside it: a step takes about
+        // 1.8 us (d = 128), an SM reads about 110 GB/s, and half of cap is taken as used.
+        const int64_t jobs = (int64_t)s.h_kv * p.pre_tiles;
+        const double steps = (double)jobs * (p.split ? 0.5 : 1.0) * ceil_div(s.P, 128);
+        const double pre_us = steps * 1.8 * s.d / 128, suf_us = 0.5 * s.B * s.h_kv * (double)s.cap * 4 * s.d / 110e3;
+        int sms = kSms;
+        if (steps >= 8 * kSms) sms -= (int)std::min(kSms * suf_us / (pre_us + suf_us), kSms / 2.0);
+        p.pre_sub = slot_keys(s.P, jobs, sms, 256);
+        // The own caches: three blocks fit an SM, ragged lengths want several rounds of them (the
+        // step above with ranges of 2048, 1024 and 512 keys: 114, 106, 110 us).
+        p.suf_sub = slot_keys(s.cap, (int64_t)s.h_kv * s.B, 8 * kSms, 256);
+    } else {  // about two blocks of 64-key tiles per SM
+        p.pre_sub = slot_keys(s.P, (int64_t)s.h_kv * p.pre_tiles, 2 * kSms, kSimtRows);
+        p.suf_sub = slot_keys(s.cap, (int64_t)s.h_kv * s.B, 2 * kSms, kSimtRows);
+    }
     p.pre_slots = p.pre_sub ? (int)ceil_div(s.P, p.pre_sub) : 0;
-    // the own caches: two blocks of four stages of 64 keys and more per SM
-    p.suf_sub = slot_keys(s.cap, (int64_t)s.h_kv * s.B, 2 * kSms, tc ? 256 : kSimtRows);
     p.suf_slots = p.suf_sub ? (int)ceil_div(s.cap, p.suf_sub) : 0;
     Carver c{nullptr};
     const size_t rows = (size_t)s.B * s.h_q * (p.pre_slots + p.suf_slots);
@@ -192,14 +244,18 @@ hsa_status_t hsa_prompt_fwd(const hsa_prompt_shape_t *shape, const void *q, cons
     if (empty) return cuda_status(cudaMemsetAsync(ws, 0, kWsHeader, st));
     cudaError_t e = cudaSuccess;  // the first launch clears the header
     const PromptWs w = carve_prompt(*shape, ws, false);
-    Args a = prompt_args(*shape, q, k, v, ws, w, row_tile(*shape));
+    Args a = prompt_args(*shape, q, k, v, ws, w, fwd_tok(*shape));
+    a.split = fwd_split(*shape);
     a.o = o;
     a.lse = lse;
     TimedLaunch tl(HSA_K_PROMPT_FWD, cu_seqlens ? 2 : 1, st);
-    if (cu_seqlens) e = launch_plan(cu_seqlens, shape->n_seq, shape->L, a.tok, false, w.plan, word(ws, kWordPlanN), a.ds, true, st);
+    if (cu_seqlens)
+        e = launch_plan(plan_job(*shape, tensor_cores(*shape) ? kRowsSplit : kRows, cu_seqlens, a.tok, w.plan, nullptr,
+                                 word(ws, kWordPlanN)),
+                        nullptr, a.ds, st);
     if (e == cudaSuccess) {
-        const int64_t items = max_items(*shape, a.tok);
-        e = shape->dtype == HSA_BF16 ? launch_fwd_tc(a, shape->d, items, word(ws, kWordNext), st)
+        const int64_t items = row_items(*shape, a.tok);
+        e = tensor_cores(*shape) ? launch_fwd_tc(a, shape->d, items, word(ws, kWordNext), st)
                                      : launch_fwd_simt(a, shape->d, items, st);
     }
     return cuda_status(e);
@@ -213,30 +269,41 @@ hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, cons
     if (s != HSA_OK) return s;
     if (!empty && !all_ok({q, k, v, o, dO, lse, dq, dk, dv})) return HSA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // the first kernel of a packed call clears the header itself
-    cudaError_t e = empty || !cu_seqlens ? cudaMemsetAsync(ws, 0, kWsHeader, st) : cudaSuccess;
-    if (empty || e != cudaSuccess) return cuda_status(e);
     const PromptWs w = carve_prompt(*shape, ws, true);
-    const bool bf16 = shape->dtype == HSA_BF16;
+    const bool planned = w.kplan != nullptr;  // the plan kernel clears the header itself
+    cudaError_t e = empty || !planned ? cudaMemsetAsync(ws, 0, kWsHeader, st) : cudaSuccess;
+    if (empty || e != cudaSuccess) return cuda_status(e);
+    const bool tc = tensor_cores(*shape);
     BwdArgs b{};
-    b.a = prompt_args(*shape, q, k, v, ws, w, bwd_row_tile(*shape));
+    b.a = prompt_args(*shape, q, k, v, ws, w, bwd_tok(*shape));
     b.kplan = w.kplan;
+    b.kpiece = w.kpiece;
     b.kplan_n = word(ws, kWordKPlanN);
-    b.ktiles = (int)ceil_div(shape->L, bwd_key_tile(*shape));
+    b.ktiles = (int)ceil_div(shape->L, key_tile(*shape));
+    b.part = w.part;
+    b.cut = w.cut;
+    b.n_cut = word(ws, kWordCutN);
     b.o = o; b.dO = dO; b.lse = lse; b.delta = w.delta;
     b.dq = dq; b.dk = dk; b.dv = dv;
-    TimedLaunch tl(HSA_K_PROMPT_BWD, cu_seqlens ? 5 : 3, st);
-    if (cu_seqlens) {
-        e = launch_plan(cu_seqlens, shape->n_seq, shape->L, b.a.tok, false, w.plan, word(ws, kWordPlanN), b.a.ds, true, st);
-        if (e == cudaSuccess)
-            e = launch_plan(cu_seqlens, shape->n_seq, shape->L, bwd_key_tile(*shape), true, w.kplan, word(ws, kWordKPlanN), b.a.ds, false, st);
+    TimedLaunch tl(HSA_K_PROMPT_BWD, 3 + planned + (w.part != nullptr), st);
+    if (planned) {
+        PlanJob keys = plan_job(*shape, tc ? kKeysSplit : kKeys, cu_seqlens, key_tile(*shape), w.kplan, w.kpiece,
+                                word(ws, kWordKPlanN));
+        keys.cut = w.cut;
+        keys.n_cut = word(ws, kWordCutN);
+        if (cu_seqlens)
+            e = launch_plan(plan_job(*shape, kRows, cu_seqlens, b.a.tok, w.plan, nullptr, word(ws, kWordPlanN)), &keys,
+                            b.a.ds, st);
+        else
+            e = launch_plan(keys, nullptr, b.a.ds, st);
     }
-    if (e == cudaSuccess) e = launch_delta(b, shape->d, bf16, st);
+    if (e == cudaSuccess) e = launch_delta(b, shape->d, tc, st);
     if (e == cudaSuccess) {
-        const int64_t row_items = max_items(*shape, b.a.tok), key_items = max_items(*shape, bwd_key_tile(*shape));
-        e = bf16 ? launch_bwd_tc(b, shape->d, row_items, key_items, word(ws, kWordNext), st)
-                 : launch_bwd_simt(b, shape->d, row_items, key_items, st);
+        const int64_t rows = row_items(*shape, b.a.tok), keys = row_items(*shape, key_tile(*shape)) + (w.part ? kMaxPieces : 0);
+        e = tc ? launch_bwd_tc(b, shape->d, rows, keys, word(ws, kWordNext), st)
+               : launch_bwd_simt(b, shape->d, rows, keys, st);
     }
+    if (e == cudaSuccess && w.part) e = launch_add_pieces(b, shape->d, st);
     return cuda_status(e);
 }
 

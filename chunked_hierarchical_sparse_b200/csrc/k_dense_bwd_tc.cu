@@ -10,7 +10,8 @@
 // (Adding 64 KB of fp32 per 128 x 128 tile pair at the 4.8 TB/s that vector
 // reductions reach on this GPU takes 2 us per SM, as long as the five products.)
 // Both keep every first operand of a second product in tensor memory:
-// - key pass: 128 keys per CTA, walking the row tiles that see them.  S^T = K Q^T
+// - key pass: 128 keys per CTA, walking the row tiles that see them (in pieces, with fp32
+//   partials added in order afterwards, where there are too few tiles for the GPU).  S^T = K Q^T
 //   and dP^T = V dO^T have a key per tensor-memory lane; p and dS go back over them
 //   as bf16 and feed dV += p dO, dK += dS Q directly.  The group's heads are rows
 //   of the same tiles, so dK and dV of shared heads are summed by the products.
@@ -68,7 +69,7 @@ template <int D> __device__ __forceinline__ void store_row(uint32_t t, float f, 
     for (int h = 0; h < D / 32; ++h) {
         float y[32];
         tmem_ld32(t + h * 32, y);
-        tmem_wait_ld();
+        wait_loads(y);
         if (real) {
             uint4 *p = reinterpret_cast<uint4 *>(dst + h * 32);
 #pragma unroll
@@ -80,12 +81,30 @@ template <int D> __device__ __forceinline__ void store_row(uint32_t t, float f, 
     }
 }
 
+// the same in fp32, unscaled
+template <int D> __device__ __forceinline__ void store_part(uint32_t t, float *dst, bool real) {
+#pragma unroll
+    for (int h = 0; h < D / 32; ++h) {
+        float y[32];
+        tmem_ld32(t + h * 32, y);
+        wait_loads(y);
+        if (real) {
+            float4 *p = reinterpret_cast<float4 *>(dst + h * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        }
+        __syncwarp();
+    }
+}
+
 struct BwdItem {
     int end, g, plane;
     int tok0, ntok;    // row pass: first token row and tokens; key pass: the sequence's first token row, its length
     int key0, nkeys;   // first key row (inside its plane) and keys
     int off;           // row pass: causal offset; key pass: first key's index in the sequence
-    int foreign, pad[7];
+    int foreign;
+    int j0, j1, slot;  // key pass: row tiles and partial slot (KeyItem)
+    int pad[4];
 };
 static_assert(sizeof(BwdItem) == 64, "item ring");
 
@@ -145,10 +164,6 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     dependents_may_start();
     const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + D;
     auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
-    // row tiles of an item: from the one that holds its first key's token to the sequence's end
-    auto first_tile = [&](const BwdItem &t) { return t.off / tt; };
-    auto end_tile = [&](const BwdItem &t) { return (t.ntok + tt - 1) / tt; };
-
     if (warp == kWarpLoad) {
         // ============================================================ items and loads
         const int total = key_item_count(b);
@@ -161,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             if (!t.end) {
                 t.g = it.g; t.plane = it.plane; t.tok0 = (int)it.row0; t.ntok = it.len;
                 t.key0 = it.start + it.n0; t.nkeys = it.nkeys; t.off = it.n0;
+                t.j0 = it.j0; t.j1 = it.j1; t.slot = it.slot;
             }
             const int ib = n % kItems;
             if (n >= kItems && !(ok = wait(&item_empty[ib], n / kItems - 1, 11))) break;
@@ -180,8 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                 }
             }
             ++fixes;
-            const int j1 = end_tile(t);
-            for (int j = first_tile(t); ok && j < j1; ++j) {
+            for (int j = t.j0; ok && j < t.j1; ++j) {
 #pragma unroll
                 for (int o = 0; o < 2; ++o) {
                     const int st = pos % L::ST;
@@ -219,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                 const BwdItem t = items[ib];
                 mbar_arrive(&item_empty[ib]);
                 if (t.end) break;
-                const int j0 = first_tile(t), j1 = end_tile(t);
+                const int j0 = t.j0, j1 = t.j1;
                 auto tile = [&](const Ring<L::ST> &r) { return smem_u32(sm + L::OFF_RING + r.st * L::TILE); };
                 // Tile j's Q or dO, as loaded next.  Rows behind the sequence's last token are
                 // another's (or nothing's): cleared, since the sums run over all 128 rows.
@@ -286,8 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             __syncwarp();
             mbar_arrive_lane0(&item_empty[ib], lane);
             if (t.end) break;
-            const int j1 = end_tile(t);
-            for (int j = first_tile(t); j < j1; ++j, ++nt) {
+            for (int j = t.j0; j < t.j1; ++j, ++nt) {
                 float l2[4], de[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -323,8 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             __syncwarp();
             mbar_arrive_lane0(&item_empty[ib], lane);
             if (t.end) break;
-            const int j1 = end_tile(t);
-            for (int j = first_tile(t); j < j1; ++j, ++nt) {
+            for (int j = t.j0; j < t.j1; ++j, ++nt) {
                 const float4 *s4 = reinterpret_cast<const float4 *>(stat + (nt & 1) * 256 + w * 64);
                 if (!(ok = wait(&stat_full[nt & 1], nt >> 1, 14))) break;
                 if (!(ok = wait(s_full, nt, 14))) break;
@@ -368,6 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             if (!ok || !(ok = wait(acc_full, na, 14))) break;
             ++na;
             tc_fence_after();
+            if (t.slot >= 0) {  // one of several pieces of this tile's rows
+                store_part<D>((w ? t_dk : t_dv) + lanes, b.part + (((int64_t)t.slot * 2 + w) * 128 + key) * D, key < t.nkeys);
+                tc_fence_before();
+                continue;
+            }
             const int64_t at = (int64_t)t.plane * a.plane[0] + (int64_t)(t.key0 + key) * D;
             if (w == 0) store_row<D>(t_dv + lanes, 1.f, static_cast<__nv_bfloat16 *>(b.dv) + at, key < t.nkeys);
             else store_row<D>(t_dk + lanes, a.scale, static_cast<__nv_bfloat16 *>(b.dk) + at, key < t.nkeys);

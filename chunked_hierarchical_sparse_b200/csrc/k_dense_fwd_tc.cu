@@ -15,10 +15,11 @@
 // run the other's products; the MMAs of a stream are issued in the order
 // P.V(j), S(j+1), so S may overwrite the P that the product before it reads, and
 // a finished S(j+1) means that O holds tiles 0..j.
-// - Prompt pass: the streams are neighbouring row tiles and share the K and V tiles.
-// - Decode, more rows than one tile: likewise.
-// - Decode, one row tile: both streams hold the same rows and take half of the keys
-//   each; their results are joined in the epilogue.
+// - Many rows: the streams are neighbouring row tiles and share the K and V tiles.
+// - Few rows (a decode batch of one row tile; a prompt whose row tiles would be too few
+//   for the GPU, or one sequence longer than its SM's share of a packed batch): both
+//   streams hold the same rows and take half of the keys each; their results are joined
+//   in the epilogue.
 // Warp 8 deals the items (dynamically, dearest first) and loads K and V by TMA, warp 9
 // issues the MMAs, warp 10 clears foreign rows, warp 11 loads Q.
 #include <algorithm>
@@ -61,9 +62,9 @@ static_assert(kItems * sizeof(TcItem) <= 256, "item ring");
 __device__ __forceinline__ bool get_tc_item(const Args &a, int i, TcItem &t) {
     Item it;
     const bool some = get_item(a, i, it);
-    const int tt = a.decode ? 128 / a.G : a.tok / 2;  // tokens of one stream's tile (shared keys)
+    const int tt = 128 / a.G;  // tokens of one stream's tile
     t.end = 0; t.plane = it.plane; t.g = it.g;
-    t.shared = !a.decode || !a.split;
+    t.shared = !it.split;
     t.foreign = it.foreign; t.slot = it.slot;
     if (t.shared) {
 #pragma unroll
@@ -81,7 +82,7 @@ __device__ __forceinline__ bool get_tc_item(const Args &a, int i, TcItem &t) {
             t.tok[s] = it.tok0;
             t.ntok[s] = it.ntok;
             t.key0[s] = it.key0 + s * half;
-            t.off[s] = kNoMask;
+            t.off[s] = it.off == kNoMask ? kNoMask : it.off - s * half;
             t.nkeys[s] = max(0, min(half, it.nkeys - s * half));
         }
     }
@@ -519,9 +520,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             const bool real = r < ntok * a.G;
             const int64_t row = ((int64_t)tok + rt) * a.hq + g * a.G + rh;
             if (!a.decode && a.off_by_one) {  // the added 1 is a logit of 0
-                const float top = fmaxf(mm, 0.f);
-                f = ex2(mm - top);
-                z = l * f + ex2(-top);
+                const float top = fmaxf(mm, 0.f), e = ex2(mm - top);
+                f *= e;
+                f1 *= e;
+                z = z * e + ex2(-top);
                 mm = top;
             }
             const float inv = z > 0.f ? f / z : (z == 0.f ? 0.f : z), inv1 = merge && z > 0.f ? f1 / z : 0.f;  // NaN stays NaN
@@ -537,28 +539,25 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                 float y[32];
                 tmem_ld32(to + h * 32, y);
                 wait_loads(y);
-                if (a.decode) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] *= inv;
-                    if (merge) {
-                        float y1[32];
-                        tmem_ld32(to + D + h * 32, y1);
-                        wait_loads(y1);
+                for (int i = 0; i < 32; ++i) y[i] *= inv;
+                if (merge) {
+                    float y1[32];
+                    tmem_ld32(to + D + h * 32, y1);
+                    wait_loads(y1);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) y[i] += y1[i] * inv1;
-                    }
+                    for (int i = 0; i < 32; ++i) y[i] += y1[i] * inv1;
+                }
+                if (real && a.decode) {
                     float4 *p = reinterpret_cast<float4 *>(a.po + prow * D + h * 32);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (real) p[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                    for (int i = 0; i < 8; ++i) p[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
                 } else if (real) {
                     uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row * D + h * 32);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        p[i] = make_uint4(bf16_pair(y[8 * i] * inv, y[8 * i + 1] * inv),
-                                          bf16_pair(y[8 * i + 2] * inv, y[8 * i + 3] * inv),
-                                          bf16_pair(y[8 * i + 4] * inv, y[8 * i + 5] * inv),
-                                          bf16_pair(y[8 * i + 6] * inv, y[8 * i + 7] * inv));
+                        p[i] = make_uint4(bf16_pair(y[8 * i], y[8 * i + 1]), bf16_pair(y[8 * i + 2], y[8 * i + 3]),
+                                          bf16_pair(y[8 * i + 4], y[8 * i + 5]), bf16_pair(y[8 * i + 6], y[8 * i + 7]));
                 }
                 __syncwarp();
             }

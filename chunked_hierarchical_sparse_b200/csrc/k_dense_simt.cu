@@ -360,7 +360,7 @@ template <typename T, int D> cudaError_t fwd(const Args &a, int64_t items, cudaS
 
 template <typename T, int D> cudaError_t delta(const BwdArgs &b, cudaStream_t st) {
     const int64_t rows = (int64_t)b.a.B * b.a.L * b.a.hq;
-    return launch_next(b.a.plan != nullptr, delta_kernel<T, D>, (int)ceil_div(rows, 8), 256, 0, st,
+    return launch_next(b.a.plan || b.kplan, delta_kernel<T, D>, (int)ceil_div(rows, 8), 256, 0, st,
                        static_cast<const T *>(b.o), static_cast<const T *>(b.dO), b.delta, rows);
 }
 

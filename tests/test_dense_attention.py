@@ -211,7 +211,7 @@ def test_waits_that_run_out_are_reported():
     try:
         codes = []
         b = {n: t.clone() for n, t in good.items()}
-        ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+        ws = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
         m.hsa_prompt_fwd(x["q"], x["k"], x["v"], o=b["o"], ws=ws)
         codes.append(m.hsa_device_status(ws))
         m.hsa_prompt_bwd(x["q"], x["k"], x["v"], good["o"], x["dO"], good["lse"], ws=ws)
