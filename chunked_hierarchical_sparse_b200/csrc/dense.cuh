@@ -170,14 +170,21 @@ struct PlanJob {
     int4 *cut;           // kKeysSplit: {first token, length, tile, slot | pieces << 16} of every cut tile
     int32_t *n_cut;
 };
-// Row tiles of a piece: half an SM's share of `work` steps, but worth its partial (8 steps).
+// A key tile whose rows are more than an SM's share of `work` steps (and an eighth, so that
+// a last round of whole tiles is not cut for nothing) is cut into pieces of at most
+// key_limit row tiles: two thirds of an SM's share, but worth their partials (4 steps).
+// (Backward of one prompt of 4K and 8K tokens, 16 heads in 2 groups: 258 and 846 us;
+// pieces of a whole share 287 and 924, of half of one 279 and 904; uncut 562 and 1262.)
 // A cut tile has fewer than 2 rows / limit pieces, so all cut tiles together have fewer
-// than 4 kPlanSms: the number of partial slots is bounded whatever the lengths are.
+// than 3 kPlanSms: the number of partial slots is bounded whatever the lengths are.
 __host__ __device__ __forceinline__ int key_limit(unsigned long long work) {
-    const unsigned long long l = (work + 2 * kPlanSms - 1) / (2 * kPlanSms);
-    return l < 8 ? 8 : l > 0x3fffffff ? 0x3fffffff : (int)l;
+    const unsigned long long l = 2 * work / (3 * kPlanSms) + 1;
+    return l < 4 ? 4 : l > 0x3fffffff ? 0x3fffffff : (int)l;
 }
-constexpr int kMaxPieces = 4 * kPlanSms;
+__host__ __device__ __forceinline__ bool cut_rows(int rows, unsigned long long work) {
+    return rows > key_limit(work) && 8ull * kPlanSms * rows > 9ull * work;
+}
+constexpr int kMaxPieces = 3 * kPlanSms;
 // words of the workspace header behind the status word
 constexpr int kHeaderWords = (int)(kWsHeader / 4), kWordPlanN = 8, kWordKPlanN = 9, kWordCutN = 10,
               kWordNext = 32;

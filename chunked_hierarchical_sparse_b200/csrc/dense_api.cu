@@ -68,7 +68,8 @@ int64_t row_items(const hsa_prompt_shape_t &s, int tok) {
 }
 
 // Forward, tensor cores, not packed: two row tiles per item where that fills the GPU, else
-// one, whose streams split the keys (4K tokens, 16 heads in 2 groups: NN us, MM without).
+// one, whose streams split the keys (one prompt of 1K
+// tokens, 16 heads in 2 groups: 16 us, 23 without).
 bool fwd_split(const hsa_prompt_shape_t &s) {
     return tensor_cores(s) && s.n_seq == 0 && row_items(s, 2 * (128 / group(s))) <= kPlanSms;
 }
@@ -90,7 +91,7 @@ uint64_t key_steps(const hsa_prompt_shape_t &s) {
 }
 bool key_pieces(const hsa_prompt_shape_t &s) {
     if (!tensor_cores(s)) return false;
-    return s.n_seq > 0 || ceil_div(s.L, 128 / group(s)) > key_limit(key_steps(s));
+    return s.n_seq > 0 || cut_rows((int)ceil_div(s.L, 128 / group(s)), key_steps(s));
 }
 
 PromptWs carve_prompt(const hsa_prompt_shape_t &s, void *ws, bool bwd) {
@@ -108,8 +109,8 @@ PromptWs carve_prompt(const hsa_prompt_shape_t &s, void *ws, bool bwd) {
             if (pieces) {
                 w.kpiece = c.take<int4>(n + kMaxPieces);
                 w.cut = c.take<int4>(std::min<int64_t>(n, kMaxPieces));
-                // pieces have more than 4 row tiles each, which bounds their number for short rows
-                const int64_t most = n * s.h_kv * (1 + ceil_div(s.L, 128 / group(s)) / 4);
+                // pieces have more than 2 row tiles, which bounds their number for short rows
+                const int64_t most = n * s.h_kv * (1 + ceil_div(s.L, 128 / group(s)) / 2);
                 w.part = c.take<float>((size_t)std::min<int64_t>(kMaxPieces, most) * 2 * 128 * s.d);
             }
         }

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                                              : 0x7fffffff;
     const int top = (J.kind == kRows || J.kind == kKeys ? (J.L + J.tok - 1) / J.tok
                      : J.kind == kRowsSplit             ? (J.L + 127) / 128
-                                                        : min(limit, (J.L + tt - 1) / tt)) + 1;
+                                                        : (J.L + tt - 1) / tt) + 1;
     // calls f(bin, tile or first token, pieces, tiles per piece) for every tile of sequence s
     auto tiles = [&](int len, auto &&f) {
         const bool halve = J.kind == kRowsSplit && (len + 127) / 128 > limit;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             if (J.kind == kRowsSplit) cost = ((min((i + 1) * tok, len) + 127) / 128 + halve) >> halve;
             if (J.kind == kKeysSplit) {
                 const int r = key_rows(i, len);
-                pieces = (r + limit - 1) / limit;
+                if (cut_rows(r, work * J.hkv)) pieces = (r + limit - 1) / limit;
                 cost = per = (r + pieces - 1) / pieces;
             }
             f(kBins - 1 - (int)min((int64_t)kBins - 1, (int64_t)cost * kBins / top), i, tok, halve, pieces, per);
