@@ -17,6 +17,11 @@
 //   of the same tiles, so dK and dV of shared heads are summed by the products.
 // - row pass: 128 (token, head) rows per CTA, walking the keys: S, dP, then
 //   dQ += dS K.  S has two buffers, so the tensor cores run ahead of the exponentials.
+// D.  Taken from the stored output (dO . o) it carries o's rounding to bf16, 2^-9 of |dO||o|,
+// into every dS of the row; that is small where a row averages many values and the largest
+// single error where it averages few.  The row pass therefore first sweeps the keys of rows
+// that have at most kSweep tiles of them for D = sum p dP (two products more per tile, on a
+// fraction of any long prompt) and leaves it to the key pass.
 // Two compute warpgroups take half of a tile's columns each (64 values of S and of dP
 // per thread); the MMAs are issued so that one warpgroup step always has one or two
 // products running behind it.
@@ -33,6 +38,10 @@ constexpr int kThreads = 384;
 constexpr int kTile = 128;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpStat = 10, kWarpClear = 11;
 constexpr int kItems = 2;
+#ifndef KSWEEP
+#define KSWEEP 4
+#endif
+constexpr int kSweep = KSWEEP;   // row pass: rows of at most so many key tiles take D from a sweep of their own
 
 template <int D, bool KEYS> struct Smem {
     static constexpr int NH = D / 64;
@@ -40,8 +49,8 @@ template <int D, bool KEYS> struct Smem {
     static constexpr int ST = KEYS ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);
     static constexpr int OFF_FIX = 0;                     // the two stationary tiles
     static constexpr int OFF_RING = 2 * TILE;
-    static constexpr int OFF_STAT = OFF_RING + ST * TILE; // key pass: [2][lse, delta][128]
-    static constexpr int OFF_ITEM = OFF_STAT + (KEYS ? 2048 : 0);
+    static constexpr int OFF_STAT = OFF_RING + ST * TILE; // key pass: [2][lse, delta][128]; row pass: [2][128]
+    static constexpr int OFF_ITEM = OFF_STAT + (KEYS ? 2048 : 1024);
     static constexpr int OFF_BAR = OFF_ITEM + kItems * 64;
     static constexpr int OFF_MISC = OFF_BAR + 512;
     static constexpr int ALLOC = OFF_MISC + 64 + 1024;    // + alignment to 1 KB
@@ -408,11 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     const Args &a = b.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *joint = reinterpret_cast<float *>(sm + L::OFF_STAT);  // [2][128]
     BwdItem *items = reinterpret_cast<BwdItem *>(sm + L::OFF_ITEM);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
     uint64_t *item_full = bar, *item_empty = bar + 2, *fix_full = bar + 4, *fix_empty = bar + 5;
     uint64_t *s_full = bar + 6, *dp_full = bar + 8, *dp_read = bar + 9, *ds_full = bar + 10, *acc_full = bar + 11;
-    uint64_t *done = bar + 12, *clean = bar + 13, *clear_req = bar + 14, *ring_full = bar + 15, *ring_empty = ring_full + L::ST;
+    uint64_t *done = bar + 12, *clean = bar + 13, *clear_req = bar + 14, *join = bar + 15, *ring_full = bar + 16, *ring_empty = ring_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
     volatile int *clear_job = abort_flag + 1;  // stage, first row
@@ -423,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
         for (int i = 0; i < 2; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 9); mbar_init(&s_full[i], 1); }
         mbar_init(fix_full, 1); mbar_init(fix_empty, 1);
         mbar_init(dp_full, 1); mbar_init(dp_read, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
+        mbar_init(join, 8);
         mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
         *abort_flag = 0;
@@ -444,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;  // S: two buffers
     auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
     auto tiles = [](int keys) { return (keys + kTile - 1) / kTile; };
+    auto sweep = [](int nt) { return nt <= kSweep ? nt : 0; };
 
     if (warp == kWarpLoad) {
         // ============================================================ items and loads
@@ -476,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                 }
             }
             ++fixes;
-            const int nt = tiles(t.nkeys);
-            for (int j = 0; ok && j < nt; ++j) {
+            const int nt = tiles(t.nkeys), all = nt + sweep(nt);
+            for (int j = 0; ok && j < all; ++j) {
 #pragma unroll
                 for (int o = 0; o < 2; ++o) {
                     const int st = pos % L::ST;
@@ -487,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
 #pragma unroll
                         for (int h = 0; h < L::NH; ++h)
                             tma_load_3d(sm + L::OFF_RING + st * L::TILE + h * 16384, o ? &tm_v : &tm_k, h * 64,
-                                        t.key0 + j * kTile, t.plane, &ring_full[st]);
+                                        t.key0 + (j < nt ? j : j - nt) * kTile, t.plane, &ring_full[st]);
                     }
                     ++pos;
                 }
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
             auto wait1 = [&](uint64_t *x, uint32_t par) { return thread_wait(x, par & 1, wait_ns, abort_flag, a.ds, 22); };
             const uint32_t qb = smem_u32(sm + L::OFF_FIX), ob = qb + L::TILE;
             Ring<L::ST> ring;
-            int nt = 0, nc = 0;
+            int nt = 0, nc = 0, nd = 0;
             bool ok = true;
             for (int n = 0; ok; ++n) {
                 const int ib = n % kItems;
@@ -516,9 +528,10 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                 mbar_arrive(&item_empty[ib]);
                 if (t.end) break;
                 if (!(ok = wait1(fix_full, n))) break;
-                const int nn = tiles(t.nkeys);
+                // steps: first the sweep for D (S and dP only), then the keys
+                const int nk = tiles(t.nkeys), sw = sweep(nk), nn = sw + nk;
                 auto tile = [&](const Ring<L::ST> &r) { return smem_u32(sm + L::OFF_RING + r.st * L::TILE); };
-                auto scores = [&](int j, Ring<L::ST> &k) -> bool {  // S of key tile j, into buffer (nt + j) & 1
+                auto scores = [&](int j, Ring<L::ST> &k) -> bool {  // S of step j, into buffer (nt + j) & 1
                     k = ring;
                     ring.next();
                     if (!wait1(&ring_full[k.st], k.ph)) return false;
@@ -530,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                     tc_fence_after();
                     mma_dots<D>(t_s + sb * 128, qb, tile(k));
                     mma_commit(&s_full[sb]);
+                    if (j < sw) mma_commit(&ring_empty[k.st]);
                     return true;
                 };
                 auto dprob = [&](int j) -> bool {
@@ -547,16 +561,19 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                 Ring<L::ST> k, kn;
                 ok = scores(0, k) && dprob(0);
                 for (int j = 0; ok && j < nn; ++j) {
+                    // (S of step j + 1 goes over that of j - 1: read, and its dS multiplied, before dP of j)
                     if (j + 1 < nn) {
                         if (!(ok = scores(j + 1, kn) && dprob(j + 1))) break;
                     } else if (!(ok = wait1(dp_read, nt + j))) {  // the next item's dP overwrites it
                         break;
                     }
-                    if (!(ok = wait1(ds_full, nt + j))) break;
-                    tc_fence_after();
-                    mma_sum<D, 64>(t_dq, t_s + ((nt + j) & 1) * 128, tile(k), j > 0);
-                    mma_commit(&ring_empty[k.st]);
-                    if (j == nn - 1) mma_commit(acc_full);
+                    if (j >= sw) {
+                        if (!(ok = wait1(ds_full, nd++))) break;
+                        tc_fence_after();
+                        mma_sum<D, 64>(t_dq, t_s + ((nt + j) & 1) * 128, tile(k), j > sw);
+                        mma_commit(&ring_empty[k.st]);
+                        if (j == nn - 1) mma_commit(acc_full);
+                    }
                     k = kn;
                 }
                 nt += nn;
@@ -577,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
         const uint32_t xd = t_dp + lanes + w * 64;
         const float c = a.scale_log2;
         const int rt = r / a.G, rh = r % a.G;
-        int nt = 0, na = 0;
+        int nt = 0, na = 0, n_join = 0;
         bool ok = true;
         for (int n = 0; ok; ++n) {
             const int ib = n % kItems;
@@ -588,10 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
             if (t.end) break;
             const bool real = r < t.ntok * a.G;
             const int64_t row = ((int64_t)t.tok0 + rt) * a.hq + t.g * a.G + rh;
-            const float l2 = real ? b.lse[row] * kLog2e : INFINITY, de = real ? b.delta[row] : 0.f;
+            const float l2 = real ? b.lse[row] * kLog2e : INFINITY;
+            float de = real ? b.delta[row] : 0.f;
             const int lim = min(t.nkeys - 1, t.off + rt), lim_all = min(t.nkeys - 1, t.off);
-            const int nn = tiles(t.nkeys);
-            for (int j = 0; j < nn; ++j, ++nt) {
+            const int nk = tiles(t.nkeys), sw = sweep(nk);
+            float dsum = 0.f;
+            for (int step = 0; step < sw + nk; ++step, ++nt) {
+                const bool first = step < sw;
+                const int j = first || !sw ? step : step - sw;
                 const int sb = nt & 1;
                 const uint32_t xs = t_s + lanes + sb * 128 + w * 64;
                 if (!(ok = wait(&s_full[sb], nt >> 1, 24))) break;
@@ -612,6 +633,35 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                 tc_fence_before();
                 __syncwarp();
                 mbar_arrive_lane0(dp_read, lane);
+                const int last = lim - j * kTile - w * 64;
+                const bool edge = j * kTile + kTile - 1 > lim_all;
+                if (first) {  // D = sum p dP over the keys this row sees
+                    float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll
+                    for (int i = 0; i < 64; i += 4) {
+                        float2 u = mul2(make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]));
+                        float2 v = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(y[i + 2], y[i + 3]));
+                        if (edge) {
+                            u.x = i <= last ? u.x : 0.f;
+                            u.y = i + 1 <= last ? u.y : 0.f;
+                            v.x = i + 2 <= last ? v.x : 0.f;
+                            v.y = i + 3 <= last ? v.y : 0.f;
+                        }
+                        a0 = add2(a0, u);
+                        a1 = add2(a1, v);
+                    }
+                    a0 = add2(a0, a1);
+                    dsum += a0.x + a0.y;
+                    if (step == sw - 1) {  // the two warpgroups' halves
+                        joint[w * 128 + r] = dsum;
+                        __syncwarp();
+                        mbar_arrive_lane0(join, lane);
+                        if (!(ok = wait(join, n_join++, 24))) break;
+                        de = joint[r] + joint[128 + r];
+                        if (w == 0 && real) b.delta[row] = de;  // for the key pass
+                    }
+                    continue;
+                }
                 const float2 d2 = make_float2(-de, -de);
 #pragma unroll
                 for (int i = 0; i < 64; i += 2) {
@@ -619,8 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                     x[i] = u.x;
                     x[i + 1] = u.y;
                 }
-                if (j * kTile + kTile - 1 > lim_all) {
-                    const int last = lim - j * kTile - w * 64;
+                if (edge) {
 #pragma unroll
                     for (int i = 0; i < 64; ++i) x[i] = i <= last ? x[i] : 0.f;
                 }
@@ -656,11 +705,12 @@ cudaError_t launch(const BwdArgs &b, int64_t row_items, int64_t key_items, int32
     cudaError_t e = set_smem_once((const void *)bwd_key_tc_kernel<D>, Smem<D, true>::ALLOC);
     if (e == cudaSuccess) e = set_smem_once((const void *)bwd_row_tc_kernel<D>, Smem<D, false>::ALLOC);
     if (e != cudaSuccess) return e;
-    e = launch_next(true, bwd_key_tc_kernel<D>, (int)std::min<int64_t>(key_items, sm_count()), kThreads,
-                    Smem<D, true>::ALLOC, st, mq, mo, mk, mv, b, next, wait_limit_ns());
+    // the row pass first: it improves delta (where it sweeps) for the key pass
+    e = launch_next(true, bwd_row_tc_kernel<D>, (int)std::min<int64_t>(row_items, sm_count()), kThreads,
+                    Smem<D, false>::ALLOC, st, mq, mo, mk, mv, b, next + 1, wait_limit_ns());
     if (e != cudaSuccess) return e;
-    return launch_next(true, bwd_row_tc_kernel<D>, (int)std::min<int64_t>(row_items, sm_count()), kThreads,
-                       Smem<D, false>::ALLOC, st, mq, mo, mk, mv, b, next + 1, wait_limit_ns());
+    return launch_next(true, bwd_key_tc_kernel<D>, (int)std::min<int64_t>(key_items, sm_count()), kThreads,
+                       Smem<D, true>::ALLOC, st, mq, mo, mk, mv, b, next, wait_limit_ns());
 }
 
 }  // namespace
