@@ -136,17 +136,24 @@ __device__ __forceinline__ void dependents_may_start() { asm volatile("griddepco
 
 template <typename... P, typename... A>
 cudaError_t launch_next(bool behind_kernel, void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t st,
-                        A &&...args) {
+                        int cluster, A &&...args) {
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)grid);
     c.blockDim = dim3((unsigned)threads);
     c.dynamicSmemBytes = smem;
     c.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = &at;
-    c.numAttrs = behind_kernel ? 1 : 0;
+    cudaLaunchAttribute at[2]{};
+    c.attrs = at;
+    if (behind_kernel) {
+        at[c.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[c.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {  // (grid is a multiple of it)
+        at[c.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[c.numAttrs].val.clusterDim.x = cluster;
+        at[c.numAttrs].val.clusterDim.y = at[c.numAttrs].val.clusterDim.z = 1;
+        ++c.numAttrs;
+    }
     return cudaLaunchKernelEx(&c, kernel, std::forward<A>(args)...);
 }
 

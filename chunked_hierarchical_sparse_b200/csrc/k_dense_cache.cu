@@ -264,7 +264,7 @@ template <int D> cudaError_t launch(const Args &a, bool first, cudaStream_t st) 
         return cudaErrorInvalidValue;
     const cudaError_t e = set_smem_once((const void *)cache_kernel<D>, Smem<D>::ALLOC);
     if (e != cudaSuccess) return e;
-    return launch_next(!first, cache_kernel<D>, a.hkv * a.B * a.suf_slots, kThreads, Smem<D>::ALLOC, st, mk, mv, a,
+    return launch_next(!first, cache_kernel<D>, a.hkv * a.B * a.suf_slots, kThreads, Smem<D>::ALLOC, st, 1, mk, mv, a,
                        (int)first, wait_limit_ns());
 }
 

@@ -588,7 +588,7 @@ cudaError_t launch(const Args &a, int64_t items, int32_t *next, cudaStream_t st)
     const int grid = (int)std::min<int64_t>(items, sm_count());
     if (!a.plan && items <= grid) next = nullptr;
     else if (!a.plan && (e = cudaMemsetAsync(a.ds, 0, kWsHeader, st)) != cudaSuccess) return e;
-    return launch_next(a.plan != nullptr, fwd_tc_kernel<D>, grid, kThreads, smem, st, mq, mk, mv, a, next,
+    return launch_next(a.plan != nullptr, fwd_tc_kernel<D>, grid, kThreads, smem, st, 1, mq, mk, mv, a, next,
                        wait_limit_ns());
 }
 

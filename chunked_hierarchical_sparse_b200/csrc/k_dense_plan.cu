@@ -247,19 +247,19 @@ template <typename T, int D> cudaError_t combine(const Args &a, cudaStream_t st)
     const bool behind = pre_items(a) + suf_items(a) > 0;  // else it is the call's first kernel
     const int rows = a.B * a.hq;
     if (rows < kJoinRows && a.pre_slots + a.suf_slots >= kJoinSlots)
-        return launch_next(behind, combine_kernel<T, D, kJoinWarps>, rows, kJoinWarps * 32, 0, st, a);
-    return launch_next(behind, combine_kernel<T, D, 1>, (rows + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, st, a);
+        return launch_next(behind, combine_kernel<T, D, kJoinWarps>, rows, kJoinWarps * 32, 0, st, 1, a);
+    return launch_next(behind, combine_kernel<T, D, 1>, (rows + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, st, 1, a);
 }
 
 }  // namespace
 
 cudaError_t launch_plan(const PlanJob &job0, const PlanJob *job1, DevStatus *ds, cudaStream_t st) {
-    return launch_next(false, plan_kernel, job1 ? 2 : 1, kPlanThreads, 0, st, job0, job1 ? *job1 : job0, ds, 1);
+    return launch_next(false, plan_kernel, job1 ? 2 : 1, kPlanThreads, 0, st, 1, job0, job1 ? *job1 : job0, ds, 1);
 }
 
 cudaError_t launch_add_pieces(const BwdArgs &b, int d, cudaStream_t st) {
-    return d == 128 ? launch_next(true, add_pieces_kernel<128>, 8 * kPlanSms, 256, 0, st, b)
-                    : launch_next(true, add_pieces_kernel<64>, 8 * kPlanSms, 256, 0, st, b);
+    return d == 128 ? launch_next(true, add_pieces_kernel<128>, 8 * kPlanSms, 256, 0, st, 1, b)
+                    : launch_next(true, add_pieces_kernel<64>, 8 * kPlanSms, 256, 0, st, 1, b);
 }
 
 cudaError_t launch_combine(const Args &a, int d, bool bf16, cudaStream_t st) {

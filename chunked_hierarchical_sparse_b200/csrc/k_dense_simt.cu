@@ -8,14 +8,23 @@
 // tile (stride d + 4 floats: 16-byte reads without bank conflicts).  Softmax state
 // (running maximum, sum, output) stays in fp32 registers.
 //
+// Few items (small problems are what fp32 is for) are shared by a cluster of C blocks, each
+// taking every C-th tile of the walk; their states are joined through distributed shared
+// memory, in rank order, each block finishing 64 / C of the rows.  No partial goes through
+// global memory and no second kernel is needed.
+//
 // Bound: FFMA issue fed by shared memory (8 16-byte reads per 64 FMAs); the tiles
 // of keys come from L2 and cost little beside it.
+#include <cooperative_groups.h>
+
 #include "dense.cuh"
 
 namespace hsa {
 namespace dense {
 
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kT = kSimtRows;
 constexpr int kThr = 256;
@@ -68,21 +77,16 @@ template <int D> __device__ __forceinline__ void dot_tile(float (&acc)[4][4], co
     }
 }
 
-// acc[i][64 h + 4 tx + e] += sum_n P(n, i) B[n][..]; P(n, i) is P[ty + 16 i][n], or P[n][ty + 16 i]
-template <int D, bool TRANSPOSED>
+// acc[i][64 h + 4 tx + e] += sum_n P[ty + 16 i][n] B[n][64 h + 4 tx + e]
+template <int D>
 __device__ __forceinline__ void accum_tile(float (&acc)[4][D / 16], const float *P, const float *B, int ty, int tx) {
 #pragma unroll 2
     for (int n = 0; n < kT; n += 4) {
         float p[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if constexpr (TRANSPOSED) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p[i][e] = P[(n + e) * kPS + ty + 16 * i];
-            } else {
-                const float4 v = *reinterpret_cast<const float4 *>(P + (ty + 16 * i) * kPS + n);
-                p[i][0] = v.x; p[i][1] = v.y; p[i][2] = v.z; p[i][3] = v.w;
-            }
+            const float4 v = *reinterpret_cast<const float4 *>(P + (ty + 16 * i) * kPS + n);
+            p[i][0] = v.x; p[i][1] = v.y; p[i][2] = v.z; p[i][3] = v.w;
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -116,6 +120,32 @@ template <typename T> __device__ __forceinline__ void store4(T *p, float4 v) {
 }
 template <> __device__ __forceinline__ void store4<float>(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
 
+// a thread's part of a 64 x d accumulator into a padded tile
+template <int D> __device__ __forceinline__ void put_tile(float *dst, const float (&acc)[4][D / 16], int ty, int tx) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+            *reinterpret_cast<float4 *>(dst + (ty + 16 * i) * (D + 4) + h * 64 + tx * 4) =
+                make_float4(acc[i][h * 4], acc[i][h * 4 + 1], acc[i][h * 4 + 2], acc[i][h * 4 + 3]);
+}
+__device__ __forceinline__ void add4(float4 &v, float4 x, float f) {
+    v.x = fmaf(f, x.x, v.x); v.y = fmaf(f, x.y, v.y); v.z = fmaf(f, x.z, v.z); v.w = fmaf(f, x.w, v.w);
+}
+// Sums a tile that every block of the cluster holds at the same place, in rank order; the
+// calling block's 64 / C rows of it go, scaled, to dst(row) + column.
+template <int D, typename T, typename F>
+__device__ __forceinline__ void add_tiles(const cg::cluster_group &cl, float *tile, int rows, float scale, F &&dst) {
+    const int C = cl.num_blocks(), rank = cl.block_rank();
+    for (int i = threadIdx.x; i < kT / C * (D / 4); i += kThr) {
+        const int r = rank * (kT / C) + i / (D / 4), c = i % (D / 4) * 4;
+        if (r >= rows) break;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = 0; q < C; ++q) add4(v, *reinterpret_cast<const float4 *>(cl.map_shared_rank(tile, q) + r * (D + 4) + c), 1.f);
+        store4<T>(dst(r) + c, make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale));
+    }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ Args a) {
     extern __shared__ float sm[];
@@ -124,7 +154,9 @@ __global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ 
     Item it;
     dependency_wait();
     dependents_may_start();
-    if ((int64_t)blockIdx.x >= item_count(a) || !get_item(a, blockIdx.x, it)) return;
+    const cg::cluster_group cl = cg::this_cluster();
+    const int rank = cl.block_rank(), C = cl.num_blocks(), item = blockIdx.x / C;
+    if (item >= item_count(a) || !get_item(a, item, it)) return;  // (the whole cluster)
     const int rows = it.ntok * a.G;
     const T *q = static_cast<const T *>(a.q);
     const T *kp = static_cast<const T *>(a.k[it.src]) + it.plane * a.plane[it.src] + (int64_t)it.key0 * D;
@@ -139,7 +171,7 @@ __global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ 
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
     }
-    for (int n0 = 0; n0 < it.nkeys; n0 += kT) {
+    for (int n0 = rank * kT; n0 < it.nkeys; n0 += C * kT) {
         __syncthreads();
         auto key = [&](const T *p, int r) -> const T * { return n0 + r < it.nkeys ? p + (int64_t)(n0 + r) * D : nullptr; };
         load_tile<D, T>(K, [&](int r) { return key(kp, r); });
@@ -173,15 +205,35 @@ __global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ 
             for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
         }
         __syncthreads();
-        accum_tile<D, false>(o, P, V, ty, tx);
+        accum_tile<D>(o, P, V, ty, tx);
     }
-    const int64_t nrow = (int64_t)a.B * a.hq;  // decode rows per slot
+    // joining the cluster: outputs and statistics in the tiles' memory
+    float *st = P;  // m[64], z[64]
+    __syncthreads();
+    put_tile<D>(K, o, ty, tx);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
-        if (r >= rows) continue;
-        const int64_t ri = row_index(r);
-        float mm = m[i] == -INFINITY ? 0.f : m[i], zz = z[i], f = 1.f;
+    for (int i = 0; i < 4; ++i)
+        if (tx == 0) {
+            st[ty + 16 * i] = m[i];
+            st[kT + ty + 16 * i] = z[i];
+        }
+    cl.sync();
+    const int64_t nrow = (int64_t)a.B * a.hq;  // decode rows per slot
+    for (int i = threadIdx.x; i < kT / C * (D / 4); i += kThr) {
+        const int r = rank * (kT / C) + i / (D / 4), c = i % (D / 4) * 4;
+        if (r >= rows) break;
+        float mm = -INFINITY;
+        for (int q2 = 0; q2 < C; ++q2) mm = fmaxf(mm, cl.map_shared_rank(st, q2)[r]);
+        if (mm == -INFINITY) mm = 0.f;
+        float zz = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q2 = 0; q2 < C; ++q2) {
+            const float *rs = cl.map_shared_rank(st, q2);
+            const float f = exp2f(rs[r] - mm);
+            zz += f * rs[kT + r];
+            add4(v, *reinterpret_cast<const float4 *>(cl.map_shared_rank(K, q2) + r * (D + 4) + c), f);
+        }
+        float f = 1.f;
         if (!a.decode && a.off_by_one) {  // the added 1 is a logit of 0
             const float top = fmaxf(mm, 0.f);
             f = exp2f(mm - top);
@@ -190,18 +242,16 @@ __global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ 
         }
         const float inv = zz > 0.f ? f / zz : (zz == 0.f ? 0.f : zz);
         const float l = (mm + log2f(zz)) * 0.6931471805599453f;
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-            const float4 v = make_float4(o[i][h * 4] * inv, o[i][h * 4 + 1] * inv, o[i][h * 4 + 2] * inv, o[i][h * 4 + 3] * inv);
-            const int c = h * 64 + tx * 4;
-            if (a.decode) store4<float>(a.po + (it.slot * nrow + ri) * D + c, v);
-            else store4<T>(static_cast<T *>(a.o) + ri * D + c, v);
-        }
-        if (tx == 0) {
+        const int64_t ri = row_index(r);
+        v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        if (a.decode) store4<float>(a.po + (it.slot * nrow + ri) * D + c, v);
+        else store4<T>(static_cast<T *>(a.o) + ri * D + c, v);
+        if (c == 0) {
             if (a.decode) a.plse[it.slot * nrow + ri] = l;
             else if (a.lse) a.lse[ri] = l;
         }
     }
+    cl.sync();  // no block leaves while another reads its memory
 }
 
 // delta[row] = dO . o, one warp per (token, head) row
@@ -226,7 +276,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const T *o, const T *dO, flo
 
 // dq of a row tile: walks the keys, dq += (p (dO.v - delta)) k
 template <typename T, int D>
-__global__ void __launch_bounds__(kThr) bwd_dq_simt_kernel(const __grid_constant__ BwdArgs b) {
+__global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dq_simt_kernel(const __grid_constant__ BwdArgs b) {
     extern __shared__ float sm[];
     const Args &a = b.a;
     float *Q = sm, *G = Q + kT * (D + 4), *K = G + kT * (D + 4), *V = K + kT * (D + 4), *S = V + kT * (D + 4);
@@ -234,7 +284,9 @@ __global__ void __launch_bounds__(kThr) bwd_dq_simt_kernel(const __grid_constant
     Item it;
     dependency_wait();
     dependents_may_start();
-    if ((int64_t)blockIdx.x >= item_count(a) || !get_item(a, blockIdx.x, it)) return;
+    const cg::cluster_group cl = cg::this_cluster();
+    const int rank = cl.block_rank(), C = cl.num_blocks(), item = blockIdx.x / C;
+    if (item >= item_count(a) || !get_item(a, item, it)) return;
     const int rows = it.ntok * a.G;
     const int64_t pl = it.plane * a.plane[0] + (int64_t)it.key0 * D;
     const T *kp = static_cast<const T *>(a.k[0]) + pl, *vp = static_cast<const T *>(a.v[0]) + pl;
@@ -250,7 +302,7 @@ __global__ void __launch_bounds__(kThr) bwd_dq_simt_kernel(const __grid_constant
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) dq[i][c] = 0.f;
     }
-    for (int n0 = 0; n0 < it.nkeys; n0 += kT) {
+    for (int n0 = rank * kT; n0 < it.nkeys; n0 += C * kT) {
         __syncthreads();
         auto key = [&](const T *p, int r) -> const T * { return n0 + r < it.nkeys ? p + (int64_t)(n0 + r) * D : nullptr; };
         load_tile<D, T>(K, [&](int r) { return key(kp, r); });
@@ -270,23 +322,18 @@ __global__ void __launch_bounds__(kThr) bwd_dq_simt_kernel(const __grid_constant
             }
         }
         __syncthreads();
-        accum_tile<D, false>(dq, S, K, ty, tx);
+        accum_tile<D>(dq, S, K, ty, tx);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
-        if (r >= rows) continue;
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-            store4<T>(static_cast<T *>(b.dq) + row_index(r) * D + h * 64 + tx * 4,
-                      make_float4(dq[i][h * 4] * a.scale, dq[i][h * 4 + 1] * a.scale, dq[i][h * 4 + 2] * a.scale,
-                                  dq[i][h * 4 + 3] * a.scale));
-    }
+    __syncthreads();
+    put_tile<D>(K, dq, ty, tx);
+    cl.sync();
+    add_tiles<D, T>(cl, K, rows, a.scale, [&](int r) { return static_cast<T *>(b.dq) + row_index(r) * D; });
+    cl.sync();
 }
 
 // dk, dv of a tile of keys: walks the row tiles that see it, all heads of the group
 template <typename T, int D>
-__global__ void __launch_bounds__(kThr) bwd_dkv_simt_kernel(const __grid_constant__ BwdArgs b) {
+__global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dkv_simt_kernel(const __grid_constant__ BwdArgs b) {
     extern __shared__ float sm[];
     const Args &a = b.a;
     float *K = sm, *V = K + kT * (D + 4), *Q = V + kT * (D + 4), *G = Q + kT * (D + 4), *P = G + kT * (D + 4),
@@ -295,7 +342,9 @@ __global__ void __launch_bounds__(kThr) bwd_dkv_simt_kernel(const __grid_constan
     KeyItem it;
     dependency_wait();
     dependents_may_start();
-    if ((int64_t)blockIdx.x >= key_item_count(b) || !get_key_item(b, blockIdx.x, kT, it)) return;
+    const cg::cluster_group cl = cg::this_cluster();
+    const int rank = cl.block_rank(), C = cl.num_blocks(), item = blockIdx.x / C;
+    if (item >= key_item_count(b) || !get_key_item(b, item, kT, it)) return;
     const int64_t pl = it.plane * a.plane[0] + (int64_t)(it.start + it.n0) * D;
     load_tile<D, T>(K, [&](int r) -> const T * { return r < it.nkeys ? static_cast<const T *>(a.k[0]) + pl + r * D : nullptr; });
     load_tile<D, T>(V, [&](int r) -> const T * { return r < it.nkeys ? static_cast<const T *>(a.v[0]) + pl + r * D : nullptr; });
@@ -304,63 +353,66 @@ __global__ void __launch_bounds__(kThr) bwd_dkv_simt_kernel(const __grid_constan
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
-    for (int t0 = it.n0; t0 < it.len; t0 += a.tok) {
+    for (int t0 = it.n0 + rank * a.tok; t0 < it.len; t0 += C * a.tok) {
         const int rows = min(a.tok, it.len - t0) * a.G;
         auto row_index = [&](int r) { return (it.row0 + t0 + r / a.G) * a.hq + it.g * a.G + r % a.G; };
         __syncthreads();
         load_tile<D, T>(Q, [&](int r) -> const T * { return r < rows ? static_cast<const T *>(a.q) + row_index(r) * D : nullptr; });
         load_tile<D, T>(G, [&](int r) -> const T * { return r < rows ? static_cast<const T *>(b.dO) + row_index(r) * D : nullptr; });
         __syncthreads();
-        float s[4][4], dp[4][4];
-        dot_tile<D>(s, Q, K, ty, tx);
-        dot_tile<D>(dp, G, V, ty, tx);
+        float s[4][4], dp[4][4];  // keys down, rows across: the sums below read P and S along their rows
+        dot_tile<D>(s, K, Q, ty, tx);
+        dot_tile<D>(dp, V, G, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = ty + 16 * i;
+        for (int j = 0; j < 4; ++j) {
+            const int r = tx + 16 * j;
             const float l2 = r < rows ? b.lse[row_index(r)] * 1.4426950408889634f : INFINITY;
             const float de = r < rows ? b.delta[row_index(r)] : 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = tx + 16 * j;
+            for (int i = 0; i < 4; ++i) {
+                const int n = ty + 16 * i;
                 const bool seen = r < rows && n < it.nkeys && it.n0 + n <= t0 + r / a.G;
                 const float p = seen ? exp2f(s[i][j] * a.scale_log2 - l2) : 0.f;
-                P[r * kPS + n] = p;
-                S[r * kPS + n] = seen ? p * (dp[i][j] - de) : 0.f;
+                P[n * kPS + r] = p;
+                S[n * kPS + r] = seen ? p * (dp[i][j] - de) : 0.f;
             }
         }
         __syncthreads();
-        accum_tile<D, true>(dv, P, G, ty, tx);
-        accum_tile<D, true>(dk, S, Q, ty, tx);
+        accum_tile<D>(dv, P, G, ty, tx);
+        accum_tile<D>(dk, S, Q, ty, tx);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = ty + 16 * i;
-        if (n >= it.nkeys) continue;
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-            const int64_t at = pl + (int64_t)n * D + h * 64 + tx * 4;
-            store4<T>(static_cast<T *>(b.dv) + at, make_float4(dv[i][h * 4], dv[i][h * 4 + 1], dv[i][h * 4 + 2], dv[i][h * 4 + 3]));
-            store4<T>(static_cast<T *>(b.dk) + at,
-                      make_float4(dk[i][h * 4] * a.scale, dk[i][h * 4 + 1] * a.scale, dk[i][h * 4 + 2] * a.scale,
-                                  dk[i][h * 4 + 3] * a.scale));
-        }
-    }
+    __syncthreads();
+    put_tile<D>(K, dv, ty, tx);
+    put_tile<D>(V, dk, ty, tx);
+    cl.sync();
+    add_tiles<D, T>(cl, K, it.nkeys, 1.f, [&](int r) { return static_cast<T *>(b.dv) + pl + (int64_t)r * D; });
+    add_tiles<D, T>(cl, V, it.nkeys, a.scale, [&](int r) { return static_cast<T *>(b.dk) + pl + (int64_t)r * D; });
+    cl.sync();
 }
 
 template <int D> constexpr size_t fwd_smem() { return sizeof(float) * (3 * kT * (D + 4) + kT * kPS); }
 template <int D> constexpr size_t dq_smem() { return sizeof(float) * (4 * kT * (D + 4) + kT * kPS); }
 template <int D> constexpr size_t dkv_smem() { return sizeof(float) * (4 * kT * (D + 4) + 2 * kT * kPS); }
 
+// Blocks per item: as many as fill the GPU about once (`fit` blocks per SM), each with a
+// tile of the walk at least
+int cluster_size(int64_t items, int walk, int fit) {
+    int c = 1;
+    while (c < 8 && items * c * 2 <= fit * kPlanSms && c * 2 <= walk) c *= 2;
+    return c;
+}
+
 template <typename T, int D> cudaError_t fwd(const Args &a, int64_t items, cudaStream_t st) {
     cudaError_t e = set_smem_once((const void *)fwd_simt_kernel<T, D>, fwd_smem<D>());
     if (e != cudaSuccess) return e;
     if (!a.plan && (e = cudaMemsetAsync(a.ds, 0, kWsHeader, st)) != cudaSuccess) return e;
-    return launch_next(a.plan != nullptr, fwd_simt_kernel<T, D>, (int)items, kThr, fwd_smem<D>(), st, a);
+    const int c = a.decode ? 1 : cluster_size(items, (int)ceil_div(a.L, kT), D == 64 ? 2 : 1);
+    return launch_next(a.plan != nullptr, fwd_simt_kernel<T, D>, (int)items * c, kThr, fwd_smem<D>(), st, c, a);
 }
 
 template <typename T, int D> cudaError_t delta(const BwdArgs &b, cudaStream_t st) {
     const int64_t rows = (int64_t)b.a.B * b.a.L * b.a.hq;
-    return launch_next(b.a.plan || b.kplan, delta_kernel<T, D>, (int)ceil_div(rows, 8), 256, 0, st,
+    return launch_next(b.a.plan || b.kplan, delta_kernel<T, D>, (int)ceil_div(rows, 8), 256, 0, st, 1,
                        static_cast<const T *>(b.o), static_cast<const T *>(b.dO), b.delta, rows);
 }
 
@@ -368,9 +420,10 @@ template <typename T, int D> cudaError_t bwd(const BwdArgs &b, int64_t row_items
     cudaError_t e = set_smem_once((const void *)bwd_dq_simt_kernel<T, D>, dq_smem<D>());
     if (e == cudaSuccess) e = set_smem_once((const void *)bwd_dkv_simt_kernel<T, D>, dkv_smem<D>());
     if (e != cudaSuccess) return e;
-    e = launch_next(true, bwd_dkv_simt_kernel<T, D>, (int)key_items, kThr, dkv_smem<D>(), st, b);
+    const int ck = cluster_size(key_items, (int)ceil_div(b.a.L, b.a.tok), D == 64 ? 2 : 1), cr = cluster_size(row_items, (int)ceil_div(b.a.L, kT), D == 64 ? 2 : 1);
+    e = launch_next(true, bwd_dkv_simt_kernel<T, D>, (int)key_items * ck, kThr, dkv_smem<D>(), st, ck, b);
     if (e != cudaSuccess) return e;
-    return launch_next(true, bwd_dq_simt_kernel<T, D>, (int)row_items, kThr, dq_smem<D>(), st, b);
+    return launch_next(true, bwd_dq_simt_kernel<T, D>, (int)row_items * cr, kThr, dq_smem<D>(), st, cr, b);
 }
 
 }  // namespace
