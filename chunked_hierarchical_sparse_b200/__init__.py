@@ -363,11 +363,14 @@ def _prefix_shape(*fields):
     return ctypes.byref(sh), int(load_library().hsa_prefix_workspace_size(ctypes.byref(sh)))
 
 
-def _out(t, name, shape, dtype, dev):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, shape, dtype, dev)
-    return t
+def _out(t, name, like, shape=None, dtype=None):
+    """The caller's output, checked, or a new one; `like`'s shape and type unless given."""
+    if t is not None:
+        _need(t, name, like.shape if shape is None else shape, dtype or like.dtype, like.device)
+        return t
+    if shape is None:
+        return torch.empty_like(like)
+    return torch.empty(tuple(shape), dtype=dtype, device=like.device)
 
 
 def _prompt_args(q, k, v, cu_seqlens, off_by_one):
@@ -411,9 +414,9 @@ def hsa_prompt_fwd(q, k, v, cu_seqlens=None, off_by_one: bool = False, want_lse:
     if n == 0:
         raise HsaError(2, "hsa_prompt_fwd")
     dev = q.device
-    o = _out(o, "o", q.shape, q.dtype, dev)
+    o = _out(o, "o", q)
     if lse is not None or want_lse:
-        lse = _out(lse, "lse", q.shape[:3], torch.float32, dev)
+        lse = _out(lse, "lse", q, q.shape[:3], torch.float32)
     w_, n = _workspace_bytes(n, dev, ws)
     _run("hsa_prompt_fwd", dev, None, sh, _p(q), _p(k), _p(v), _p(cu_seqlens), _p(o), _p(lse), _p(w_), n)
     return o, lse
@@ -432,9 +435,7 @@ def hsa_prompt_bwd(q, k, v, o, dO, lse, cu_seqlens=None, dq=None, dk=None, dv=No
     _need(o, "o", q.shape, q.dtype, dev)
     _need(dO, "dO", q.shape, q.dtype, dev)
     _need(lse, "lse", q.shape[:3], torch.float32, dev)
-    dq = _out(dq, "dq", q.shape, q.dtype, dev)
-    dk = _out(dk, "dk", k.shape, q.dtype, dev)
-    dv = _out(dv, "dv", v.shape, q.dtype, dev)
+    dq, dk, dv = _out(dq, "dq", q), _out(dk, "dk", k), _out(dv, "dv", k)
     w_, n = _workspace_bytes(n, dev, ws)
     _run("hsa_prompt_bwd", dev, None, sh, _p(q), _p(k), _p(v), _p(o), _p(dO), _p(lse), _p(cu_seqlens), _p(dq),
          _p(dk), _p(dv), _p(w_), n)
@@ -489,9 +490,9 @@ def hsa_prefix_decode(q, k_prefix, v_prefix, k_cache, v_cache, lens, off_by_one:
     sh, n = _prefix_shape(B, k_prefix.shape[1], cap, h_q, h_kv, d, 1 if off_by_one else 0, dt, stride)
     if n == 0:
         raise HsaError(2, "hsa_prefix_decode")
-    o = _out(o, "o", q.shape, q.dtype, dev)
+    o = _out(o, "o", q)
     if lse is not None or want_lse:
-        lse = _out(lse, "lse", (B, h_q), torch.float32, dev)
+        lse = _out(lse, "lse", q, (B, h_q), torch.float32)
     w_, n = _workspace_bytes(n, dev, ws)
     _run("hsa_prefix_decode", dev, None, sh, _p(q), _p(k_prefix), _p(v_prefix), _p(k_cache), _p(v_cache), _p(lens),
          _p(o), _p(lse), _p(w_), n)

@@ -286,7 +286,7 @@ hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, cons
     b.n_cut = word(ws, kWordCutN);
     b.o = o; b.dO = dO; b.lse = lse; b.delta = w.delta;
     b.dq = dq; b.dk = dk; b.dv = dv;
-    TimedLaunch tl(HSA_K_PROMPT_BWD, 3 + planned + (w.part != nullptr), st);
+    TimedLaunch tl(HSA_K_PROMPT_BWD, (tc ? 2 : 3) + planned + (w.part != nullptr), st);
     if (planned) {
         PlanJob keys = plan_job(*shape, tc ? kKeysSplit : kKeys, cu_seqlens, key_tile(*shape), w.kplan, w.kpiece,
                                 word(ws, kWordKPlanN));
@@ -298,7 +298,7 @@ hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, cons
         else
             e = launch_plan(keys, nullptr, b.a.ds, st);
     }
-    if (e == cudaSuccess) e = launch_delta(b, shape->d, tc, st);
+    if (e == cudaSuccess && !tc) e = launch_delta(b, shape->d, st);
     if (e == cudaSuccess) {
         const int64_t rows = row_items(*shape, b.a.tok), keys = row_items(*shape, key_tile(*shape)) + (w.part ? kMaxPieces : 0);
         e = tc ? launch_bwd_tc(b, shape->d, rows, keys, word(ws, kWordNext), st)

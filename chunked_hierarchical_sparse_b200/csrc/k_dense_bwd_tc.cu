@@ -17,7 +17,7 @@
 //   of the same tiles, so dK and dV of shared heads are summed by the products.
 // - row pass: 128 (token, head) rows per CTA, walking the keys: S, dP, then
 //   dQ += dS K.  S has two buffers, so the tensor cores run ahead of the exponentials.
-// D.  Taken from the stored output (dO . o) it carries o's rounding to bf16, 2^-9 of |dO||o|,
+// D (written by the row pass, which goes first).  Taken from the stored output (dO . o) it carries o's rounding to bf16, 2^-9 of |dO||o|,
 // into every dS of the row; that is small where a row averages many values and the largest
 // single error where it averages few.  The row pass therefore first sweeps the keys of rows
 // that have at most kSweep tiles of them for D = sum p dP (two products more per tile, on a
@@ -70,6 +70,13 @@ __device__ __forceinline__ void store64(uint32_t t, const float (&x)[64]) {  // 
     for (int i = 0; i < 32; ++i) u[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
     tmem_st32(t, u);
     tmem_wait_st();
+}
+__device__ __forceinline__ float dot8(uint4 a, uint4 b) {  // eight bf16 products
+    auto two = [](uint32_t x, uint32_t y) {
+        return __uint_as_float(x << 16) * __uint_as_float(y << 16) +
+               __uint_as_float(x & 0xffff0000u) * __uint_as_float(y & 0xffff0000u);
+    };
+    return (two(a.x, b.x) + two(a.y, b.y)) + (two(a.z, b.z) + two(a.w, b.w));
 }
 // one row of a [128 x d] accumulator, scaled, to global memory
 template <int D> __device__ __forceinline__ void store_row(uint32_t t, float f, __nv_bfloat16 *dst, bool real) {
@@ -605,10 +612,24 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
             const bool real = r < t.ntok * a.G;
             const int64_t row = ((int64_t)t.tok0 + rt) * a.hq + t.g * a.G + rh;
             const float l2 = real ? b.lse[row] * kLog2e : INFINITY;
-            float de = real ? b.delta[row] : 0.f;
+            float de = 0.f;
             const int lim = min(t.nkeys - 1, t.off + rt), lim_all = min(t.nkeys - 1, t.off);
             const int nk = tiles(t.nkeys), sw = sweep(nk);
             float dsum = 0.f;
+            if (!sw && real) {  // D = dO . o, half of the columns per warpgroup
+                const uint4 *po = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(b.o) + row * D + w * (D / 2));
+                const uint4 *pd = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(b.dO) + row * D + w * (D / 2));
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) dsum += dot8(po[i], pd[i]);
+            }
+            if (!sw) {
+                joint[w * 128 + r] = dsum;
+                __syncwarp();
+                mbar_arrive_lane0(join, lane);
+                if (!(ok = wait(join, n_join++, 24))) break;
+                de = joint[r] + joint[128 + r];
+                if (w == 0 && real) b.delta[row] = de;  // for the key pass
+            }
             for (int step = 0; step < sw + nk; ++step, ++nt) {
                 const bool first = step < sw;
                 const int j = first || !sw ? step : step - sw;
@@ -657,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                         mbar_arrive_lane0(join, lane);
                         if (!(ok = wait(join, n_join++, 24))) break;
                         de = joint[r] + joint[128 + r];
-                        if (w == 0 && real) b.delta[row] = de;  // for the key pass
+                        if (w == 0 && real) b.delta[row] = de;
                     }
                     continue;
                 }
@@ -704,8 +725,8 @@ cudaError_t launch(const BwdArgs &b, int64_t row_items, int64_t key_items, int32
     cudaError_t e = set_smem_once((const void *)bwd_key_tc_kernel<D>, Smem<D, true>::ALLOC);
     if (e == cudaSuccess) e = set_smem_once((const void *)bwd_row_tc_kernel<D>, Smem<D, false>::ALLOC);
     if (e != cudaSuccess) return e;
-    // the row pass first: it improves delta (where it sweeps) for the key pass
-    e = launch_next(true, bwd_row_tc_kernel<D>, (int)std::min<int64_t>(row_items, sm_count()), kThreads,
+    // the row pass first: it writes delta for the key pass
+    e = launch_next(b.a.plan || b.kplan, bwd_row_tc_kernel<D>, (int)std::min<int64_t>(row_items, sm_count()), kThreads,
                     Smem<D, false>::ALLOC, st, 1, mq, mo, mk, mv, b, next + 1, wait_limit_ns());
     if (e != cudaSuccess) return e;
     return launch_next(true, bwd_key_tc_kernel<D>, (int)std::min<int64_t>(key_items, sm_count()), kThreads,

@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __shared__ int warp_sum[kPlanThreads / 32];
     __shared__ int bad, slots, cuts;
     __shared__ unsigned long long work;
+    __shared__ int bounds[kPlanThreads + 1];  // cu, where it fits: read once
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     hist[tid] = 0;
     if (tid == 0) {
@@ -35,13 +36,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __syncthreads();
     dependents_may_start();
     const int tt = 128 / J.G;  // tokens of a 128-row tile
+    const bool fits = J.n_seq <= kPlanThreads;
+    auto bound = [&](int s) { return fits ? bounds[s] : J.cu[s]; };
     auto seq = [&](int s, int &a, int &len) {
-        a = J.cu ? J.cu[s] : s * J.L;
-        len = J.cu ? J.cu[s + 1] - a : J.L;
+        a = J.cu ? bound(s) : s * J.L;
+        len = J.cu ? bound(s + 1) - a : J.L;
     };
     auto key_rows = [&](int i, int len) { return (len + tt - 1) / tt - i * 128 / tt; };  // row tiles that see key tile i
+    if (J.cu && fits) {
+        for (int s = tid; s <= J.n_seq; s += kPlanThreads) bounds[s] = J.cu[s];
+        __syncthreads();
+    }
     for (int s = tid; J.cu && s < J.n_seq; s += kPlanThreads) {
-        const int a = J.cu[s], b = J.cu[s + 1];
+        const int a = bound(s), b = bound(s + 1);
         if (a < 0 || b < a || b > J.L) {
             bad = 1;
             report(ds, HSA_ERR_DEVICE_CHECK, kKDense, s, b);

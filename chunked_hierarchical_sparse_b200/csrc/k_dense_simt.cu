@@ -1,4 +1,4 @@
-// k_dense_simt.cu -- dense attention and its backward on the CUDA cores.
+// k_dense_simt.cu -- dense attention and its backward in fp32, on the CUDA cores.
 //
 // A block takes one tile of 64 (token, head) rows of a group and walks the keys
 // in tiles of 64 (the key-major backward kernel: a tile of 64 keys, walking the
@@ -30,23 +30,13 @@ constexpr int kT = kSimtRows;
 constexpr int kThr = 256;
 constexpr int kPS = kT + 4;  // row stride of a 64 x 64 tile
 
-template <typename T> __device__ __forceinline__ float4 load4(const T *p);
-template <> __device__ __forceinline__ float4 load4<float>(const float *p) {
-    return *reinterpret_cast<const float4 *>(p);
-}
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-}
-
 // 64 rows of d values into a padded tile; row r comes from src(r) (null: zeros)
-template <int D, typename T, typename F> __device__ __forceinline__ void load_tile(float *dst, F &&src) {
+template <int D, typename F> __device__ __forceinline__ void load_tile(float *dst, F &&src) {
     constexpr int V = D / 4;
     for (int i = threadIdx.x; i < kT * V; i += kThr) {
         const int r = i / V, c = (i % V) * 4;
-        const T *p = src(r);
-        const float4 x = p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float *p = src(r);
+        const float4 x = p ? *reinterpret_cast<const float4 *>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
         *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = x;
     }
 }
@@ -115,10 +105,7 @@ __device__ __forceinline__ float row_sum16(float x) {
     return x;
 }
 
-template <typename T> __device__ __forceinline__ void store4(T *p, float4 v) {
-    Elem<T>::store(p, v.x); Elem<T>::store(p + 1, v.y); Elem<T>::store(p + 2, v.z); Elem<T>::store(p + 3, v.w);
-}
-template <> __device__ __forceinline__ void store4<float>(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
 
 // a thread's part of a 64 x d accumulator into a padded tile
 template <int D> __device__ __forceinline__ void put_tile(float *dst, const float (&acc)[4][D / 16], int ty, int tx) {
@@ -134,7 +121,7 @@ __device__ __forceinline__ void add4(float4 &v, float4 x, float f) {
 }
 // Sums a tile that every block of the cluster holds at the same place, in rank order; the
 // calling block's 64 / C rows of it go, scaled, to dst(row) + column.
-template <int D, typename T, typename F>
+template <int D, typename F>
 __device__ __forceinline__ void add_tiles(const cg::cluster_group &cl, float *tile, int rows, float scale, F &&dst) {
     const int C = cl.num_blocks(), rank = cl.block_rank();
     for (int i = threadIdx.x; i < kT / C * (D / 4); i += kThr) {
@@ -142,11 +129,11 @@ __device__ __forceinline__ void add_tiles(const cg::cluster_group &cl, float *ti
         if (r >= rows) break;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int q = 0; q < C; ++q) add4(v, *reinterpret_cast<const float4 *>(cl.map_shared_rank(tile, q) + r * (D + 4) + c), 1.f);
-        store4<T>(dst(r) + c, make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale));
+        store4(dst(r) + c, make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale));
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ Args a) {
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + kT * (D + 4), *V = K + kT * (D + 4), *P = V + kT * (D + 4);
@@ -158,11 +145,11 @@ __global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ 
     const int rank = cl.block_rank(), C = cl.num_blocks(), item = blockIdx.x / C;
     if (item >= item_count(a) || !get_item(a, item, it)) return;  // (the whole cluster)
     const int rows = it.ntok * a.G;
-    const T *q = static_cast<const T *>(a.q);
-    const T *kp = static_cast<const T *>(a.k[it.src]) + it.plane * a.plane[it.src] + (int64_t)it.key0 * D;
-    const T *vp = static_cast<const T *>(a.v[it.src]) + it.plane * a.plane[it.src] + (int64_t)it.key0 * D;
+    const float *q = static_cast<const float *>(a.q);
+    const float *kp = static_cast<const float *>(a.k[it.src]) + it.plane * a.plane[it.src] + (int64_t)it.key0 * D;
+    const float *vp = static_cast<const float *>(a.v[it.src]) + it.plane * a.plane[it.src] + (int64_t)it.key0 * D;
     auto row_index = [&](int r) { return ((int64_t)it.tok0 + r / a.G) * a.hq + it.g * a.G + r % a.G; };
-    load_tile<D, T>(Q, [&](int r) -> const T * { return r < rows ? q + row_index(r) * D : nullptr; });
+    load_tile<D>(Q, [&](int r) -> const float * { return r < rows ? q + row_index(r) * D : nullptr; });
     float m[4], z[4], o[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -173,9 +160,9 @@ __global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ 
     }
     for (int n0 = rank * kT; n0 < it.nkeys; n0 += C * kT) {
         __syncthreads();
-        auto key = [&](const T *p, int r) -> const T * { return n0 + r < it.nkeys ? p + (int64_t)(n0 + r) * D : nullptr; };
-        load_tile<D, T>(K, [&](int r) { return key(kp, r); });
-        load_tile<D, T>(V, [&](int r) { return key(vp, r); });
+        auto key = [&](const float *p, int r) -> const float * { return n0 + r < it.nkeys ? p + (int64_t)(n0 + r) * D : nullptr; };
+        load_tile<D>(K, [&](int r) { return key(kp, r); });
+        load_tile<D>(V, [&](int r) { return key(vp, r); });
         __syncthreads();
         float s[4][4];
         dot_tile<D>(s, Q, K, ty, tx);
@@ -244,8 +231,8 @@ __global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ 
         const float l = (mm + log2f(zz)) * 0.6931471805599453f;
         const int64_t ri = row_index(r);
         v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-        if (a.decode) store4<float>(a.po + (it.slot * nrow + ri) * D + c, v);
-        else store4<T>(static_cast<T *>(a.o) + ri * D + c, v);
+        if (a.decode) store4(a.po + (it.slot * nrow + ri) * D + c, v);
+        else store4(static_cast<float *>(a.o) + ri * D + c, v);
         if (c == 0) {
             if (a.decode) a.plse[it.slot * nrow + ri] = l;
             else if (a.lse) a.lse[ri] = l;
@@ -255,8 +242,8 @@ __global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ 
 }
 
 // delta[row] = dO . o, one warp per (token, head) row
-template <typename T, int D>
-__global__ void __launch_bounds__(256) delta_kernel(const T *o, const T *dO, float *delta, int64_t rows) {
+template <int D>
+__global__ void __launch_bounds__(256) delta_kernel(const float *o, const float *dO, float *delta, int64_t rows) {
     const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     dependency_wait();
@@ -266,7 +253,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const T *o, const T *dO, flo
 #pragma unroll
     for (int c = 0; c < D; c += 128) {
         if (c + lane * 4 < D) {
-            const float4 x = load4<T>(o + r * D + c + lane * 4), y = load4<T>(dO + r * D + c + lane * 4);
+            const float4 x = *reinterpret_cast<const float4 *>(o + r * D + c + lane * 4), y = *reinterpret_cast<const float4 *>(dO + r * D + c + lane * 4);
             s += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
         }
     }
@@ -275,7 +262,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const T *o, const T *dO, flo
 }
 
 // dq of a row tile: walks the keys, dq += (p (dO.v - delta)) k
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dq_simt_kernel(const __grid_constant__ BwdArgs b) {
     extern __shared__ float sm[];
     const Args &a = b.a;
@@ -289,10 +276,10 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dq_simt_kernel(cons
     if (item >= item_count(a) || !get_item(a, item, it)) return;
     const int rows = it.ntok * a.G;
     const int64_t pl = it.plane * a.plane[0] + (int64_t)it.key0 * D;
-    const T *kp = static_cast<const T *>(a.k[0]) + pl, *vp = static_cast<const T *>(a.v[0]) + pl;
+    const float *kp = static_cast<const float *>(a.k[0]) + pl, *vp = static_cast<const float *>(a.v[0]) + pl;
     auto row_index = [&](int r) { return ((int64_t)it.tok0 + r / a.G) * a.hq + it.g * a.G + r % a.G; };
-    load_tile<D, T>(Q, [&](int r) -> const T * { return r < rows ? static_cast<const T *>(a.q) + row_index(r) * D : nullptr; });
-    load_tile<D, T>(G, [&](int r) -> const T * { return r < rows ? static_cast<const T *>(b.dO) + row_index(r) * D : nullptr; });
+    load_tile<D>(Q, [&](int r) -> const float * { return r < rows ? static_cast<const float *>(a.q) + row_index(r) * D : nullptr; });
+    load_tile<D>(G, [&](int r) -> const float * { return r < rows ? static_cast<const float *>(b.dO) + row_index(r) * D : nullptr; });
     float l2[4], de[4], dq[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -304,9 +291,9 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dq_simt_kernel(cons
     }
     for (int n0 = rank * kT; n0 < it.nkeys; n0 += C * kT) {
         __syncthreads();
-        auto key = [&](const T *p, int r) -> const T * { return n0 + r < it.nkeys ? p + (int64_t)(n0 + r) * D : nullptr; };
-        load_tile<D, T>(K, [&](int r) { return key(kp, r); });
-        load_tile<D, T>(V, [&](int r) { return key(vp, r); });
+        auto key = [&](const float *p, int r) -> const float * { return n0 + r < it.nkeys ? p + (int64_t)(n0 + r) * D : nullptr; };
+        load_tile<D>(K, [&](int r) { return key(kp, r); });
+        load_tile<D>(V, [&](int r) { return key(vp, r); });
         __syncthreads();
         float s[4][4], dp[4][4];
         dot_tile<D>(s, Q, K, ty, tx);
@@ -327,12 +314,12 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dq_simt_kernel(cons
     __syncthreads();
     put_tile<D>(K, dq, ty, tx);
     cl.sync();
-    add_tiles<D, T>(cl, K, rows, a.scale, [&](int r) { return static_cast<T *>(b.dq) + row_index(r) * D; });
+    add_tiles<D>(cl, K, rows, a.scale, [&](int r) { return static_cast<float *>(b.dq) + row_index(r) * D; });
     cl.sync();
 }
 
 // dk, dv of a tile of keys: walks the row tiles that see it, all heads of the group
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dkv_simt_kernel(const __grid_constant__ BwdArgs b) {
     extern __shared__ float sm[];
     const Args &a = b.a;
@@ -346,8 +333,8 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dkv_simt_kernel(con
     const int rank = cl.block_rank(), C = cl.num_blocks(), item = blockIdx.x / C;
     if (item >= key_item_count(b) || !get_key_item(b, item, kT, it)) return;
     const int64_t pl = it.plane * a.plane[0] + (int64_t)(it.start + it.n0) * D;
-    load_tile<D, T>(K, [&](int r) -> const T * { return r < it.nkeys ? static_cast<const T *>(a.k[0]) + pl + r * D : nullptr; });
-    load_tile<D, T>(V, [&](int r) -> const T * { return r < it.nkeys ? static_cast<const T *>(a.v[0]) + pl + r * D : nullptr; });
+    load_tile<D>(K, [&](int r) -> const float * { return r < it.nkeys ? static_cast<const float *>(a.k[0]) + pl + r * D : nullptr; });
+    load_tile<D>(V, [&](int r) -> const float * { return r < it.nkeys ? static_cast<const float *>(a.v[0]) + pl + r * D : nullptr; });
     float dk[4][D / 16], dv[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -357,8 +344,8 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dkv_simt_kernel(con
         const int rows = min(a.tok, it.len - t0) * a.G;
         auto row_index = [&](int r) { return (it.row0 + t0 + r / a.G) * a.hq + it.g * a.G + r % a.G; };
         __syncthreads();
-        load_tile<D, T>(Q, [&](int r) -> const T * { return r < rows ? static_cast<const T *>(a.q) + row_index(r) * D : nullptr; });
-        load_tile<D, T>(G, [&](int r) -> const T * { return r < rows ? static_cast<const T *>(b.dO) + row_index(r) * D : nullptr; });
+        load_tile<D>(Q, [&](int r) -> const float * { return r < rows ? static_cast<const float *>(a.q) + row_index(r) * D : nullptr; });
+        load_tile<D>(G, [&](int r) -> const float * { return r < rows ? static_cast<const float *>(b.dO) + row_index(r) * D : nullptr; });
         __syncthreads();
         float s[4][4], dp[4][4];  // keys down, rows across: the sums below read P and S along their rows
         dot_tile<D>(s, K, Q, ty, tx);
@@ -385,8 +372,8 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dkv_simt_kernel(con
     put_tile<D>(K, dv, ty, tx);
     put_tile<D>(V, dk, ty, tx);
     cl.sync();
-    add_tiles<D, T>(cl, K, it.nkeys, 1.f, [&](int r) { return static_cast<T *>(b.dv) + pl + (int64_t)r * D; });
-    add_tiles<D, T>(cl, V, it.nkeys, a.scale, [&](int r) { return static_cast<T *>(b.dk) + pl + (int64_t)r * D; });
+    add_tiles<D>(cl, K, it.nkeys, 1.f, [&](int r) { return static_cast<float *>(b.dv) + pl + (int64_t)r * D; });
+    add_tiles<D>(cl, V, it.nkeys, a.scale, [&](int r) { return static_cast<float *>(b.dk) + pl + (int64_t)r * D; });
     cl.sync();
 }
 
@@ -402,43 +389,42 @@ int cluster_size(int64_t items, int walk, int fit) {
     return c;
 }
 
-template <typename T, int D> cudaError_t fwd(const Args &a, int64_t items, cudaStream_t st) {
-    cudaError_t e = set_smem_once((const void *)fwd_simt_kernel<T, D>, fwd_smem<D>());
+template <int D> cudaError_t fwd(const Args &a, int64_t items, cudaStream_t st) {
+    cudaError_t e = set_smem_once((const void *)fwd_simt_kernel<D>, fwd_smem<D>());
     if (e != cudaSuccess) return e;
     if (!a.plan && (e = cudaMemsetAsync(a.ds, 0, kWsHeader, st)) != cudaSuccess) return e;
     const int c = a.decode ? 1 : cluster_size(items, (int)ceil_div(a.L, kT), D == 64 ? 2 : 1);
-    return launch_next(a.plan != nullptr, fwd_simt_kernel<T, D>, (int)items * c, kThr, fwd_smem<D>(), st, c, a);
+    return launch_next(a.plan != nullptr, fwd_simt_kernel<D>, (int)items * c, kThr, fwd_smem<D>(), st, c, a);
 }
 
-template <typename T, int D> cudaError_t delta(const BwdArgs &b, cudaStream_t st) {
+template <int D> cudaError_t delta(const BwdArgs &b, cudaStream_t st) {
     const int64_t rows = (int64_t)b.a.B * b.a.L * b.a.hq;
-    return launch_next(b.a.plan || b.kplan, delta_kernel<T, D>, (int)ceil_div(rows, 8), 256, 0, st, 1,
-                       static_cast<const T *>(b.o), static_cast<const T *>(b.dO), b.delta, rows);
+    return launch_next(b.a.plan || b.kplan, delta_kernel<D>, (int)ceil_div(rows, 8), 256, 0, st, 1,
+                       static_cast<const float *>(b.o), static_cast<const float *>(b.dO), b.delta, rows);
 }
 
-template <typename T, int D> cudaError_t bwd(const BwdArgs &b, int64_t row_items, int64_t key_items, cudaStream_t st) {
-    cudaError_t e = set_smem_once((const void *)bwd_dq_simt_kernel<T, D>, dq_smem<D>());
-    if (e == cudaSuccess) e = set_smem_once((const void *)bwd_dkv_simt_kernel<T, D>, dkv_smem<D>());
+template <int D> cudaError_t bwd(const BwdArgs &b, int64_t row_items, int64_t key_items, cudaStream_t st) {
+    cudaError_t e = set_smem_once((const void *)bwd_dq_simt_kernel<D>, dq_smem<D>());
+    if (e == cudaSuccess) e = set_smem_once((const void *)bwd_dkv_simt_kernel<D>, dkv_smem<D>());
     if (e != cudaSuccess) return e;
     const int ck = cluster_size(key_items, (int)ceil_div(b.a.L, b.a.tok), D == 64 ? 2 : 1), cr = cluster_size(row_items, (int)ceil_div(b.a.L, kT), D == 64 ? 2 : 1);
-    e = launch_next(true, bwd_dkv_simt_kernel<T, D>, (int)key_items * ck, kThr, dkv_smem<D>(), st, ck, b);
+    e = launch_next(true, bwd_dkv_simt_kernel<D>, (int)key_items * ck, kThr, dkv_smem<D>(), st, ck, b);
     if (e != cudaSuccess) return e;
-    return launch_next(true, bwd_dq_simt_kernel<T, D>, (int)row_items * cr, kThr, dq_smem<D>(), st, cr, b);
+    return launch_next(true, bwd_dq_simt_kernel<D>, (int)row_items * cr, kThr, dq_smem<D>(), st, cr, b);
 }
 
 }  // namespace
 
 cudaError_t launch_fwd_simt(const Args &a, int d, int64_t items, cudaStream_t st) {
-    return d == 128 ? fwd<float, 128>(a, items, st) : fwd<float, 64>(a, items, st);
+    return d == 128 ? fwd<128>(a, items, st) : fwd<64>(a, items, st);
 }
 
-cudaError_t launch_delta(const BwdArgs &b, int d, bool bf16, cudaStream_t st) {
-    if (bf16) return d == 128 ? delta<__nv_bfloat16, 128>(b, st) : delta<__nv_bfloat16, 64>(b, st);
-    return d == 128 ? delta<float, 128>(b, st) : delta<float, 64>(b, st);
+cudaError_t launch_delta(const BwdArgs &b, int d, cudaStream_t st) {
+    return d == 128 ? delta<128>(b, st) : delta<64>(b, st);
 }
 
 cudaError_t launch_bwd_simt(const BwdArgs &b, int d, int64_t row_items, int64_t key_items, cudaStream_t st) {
-    return d == 128 ? bwd<float, 128>(b, row_items, key_items, st) : bwd<float, 64>(b, row_items, key_items, st);
+    return d == 128 ? bwd<128>(b, row_items, key_items, st) : bwd<64>(b, row_items, key_items, st);
 }
 
 }  // namespace dense
