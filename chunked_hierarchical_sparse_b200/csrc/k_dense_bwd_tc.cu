@@ -23,7 +23,7 @@
 // that have at most kSweep tiles of them for D = sum p dP (two products more per tile, on a
 // fraction of any long prompt) and leaves it to the key pass.  Relative error of dq against 64
 // bits: prompts of 12 tokens 0.0031 -> 0.0025, 16K tokens 0.0026 -> 0.0024 (rounding dq alone:
-// 0.0017; eight tiles instead of four gain 0.00001), for 2 to 5 us a call.
+// 0.0017; eight tiles instead of two gain 0.00002), for about 2 us a call.
 // Two compute warpgroups take half of a tile's columns each (64 values of S and of dP
 // per thread); the MMAs are issued so that one warpgroup step always has one or two
 // products running behind it.
@@ -40,7 +40,7 @@ constexpr int kThreads = 384;
 constexpr int kTile = 128;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpStat = 10, kWarpClear = 11;
 constexpr int kItems = 2;
-constexpr int kSweep = 4;   // row pass: rows of at most so many key tiles take D from a sweep of their own
+constexpr int kSweep = 2;   // row pass: rows of at most so many key tiles take D from a sweep of their own
 
 template <int D, bool KEYS> struct Smem {
     static constexpr int NH = D / 64;

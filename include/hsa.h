@@ -203,11 +203,14 @@ HSA_API hsa_status_t hsa_bwd(const hsa_shape_t *shape, const void *q, const void
  * Z_t = 1 + sum_j e^{x_tj} (softmax-off-by-one, as inside a chunk of hsa_fwd).
  * o_t = sum_j e^{x_tj} v_j / Z_t and lse_t = log Z_t.  A row without any key has
  * o = 0 and lse = log Z (-infinity, or 0 with off_by_one).
- * d in {64, 128}, h_q % h_kv == 0, h_q / h_kv <= 16, fp32 or bf16.  Logits,
- * softmax statistics and all sums are fp32; in bf16 the probabilities (and, in
- * the backward, their gradients) are rounded to bf16 as operands of the second
- * product, the usual choice for tensor cores.  Results are the same bit for bit
- * on every call. */
+ * d in {64, 128}, h_q % h_kv == 0, h_q / h_kv <= 16, fp32 or bf16; the prompt
+ * pass takes B * L < 2^30 and (B * L + n_seq) * h_kv < 2^30, the decode step
+ * B * h_q < 2^24 and P, cap < 2^30.  Outputs may not overlap inputs.
+ *
+ * Logits, softmax statistics and all sums are fp32.  In bf16 the probabilities
+ * (and, in the backward, their gradients) are rounded to bf16 once, as operands of
+ * the second product: the tensor cores multiply operands of one type, and the
+ * values they meet are bf16 too.  Results are the same bit for bit on every call. */
 
 typedef struct {
     int32_t B;          /* batch rows                                            */
@@ -242,7 +245,8 @@ HSA_API hsa_status_t hsa_prompt_fwd(const hsa_prompt_shape_t *shape, const void 
 
 /* Backward of hsa_prompt_fwd: gradients of sum(dO * o), from its inputs and its
  * o and lse (which carry off_by_one).  dq [B,L,h_q,d], dk, dv [B,h_kv,L,d], all
- * required; rows outside every sequence are neither read nor written. */
+ * required; rows outside every sequence are neither read nor written.  A NaN or
+ * infinity at a token reaches gradients of its own sequence only. */
 HSA_API hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, const void *k,
                                     const void *v, const void *o, const void *dO, const float *lse,
                                     const int32_t *cu_seqlens, void *dq, void *dk, void *dv, void *ws,
