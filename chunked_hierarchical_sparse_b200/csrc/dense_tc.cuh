@@ -107,6 +107,58 @@ __device__ __forceinline__ void wait_loads(float (&x)[32]) {
                  : "memory");
 }
 
+// Rows that the lanes of a warp hold one each (64 bytes at a time) go to global memory in
+// pieces of 16 bytes that the four lanes of a quad first exchange, so that a store writes
+// 64 consecutive bytes of 8 rows instead of 16 bytes of 32: the load/store unit takes a
+// cycle per 128-byte line, and a direct store of a 128 x 128 tile keeps it for 2000.
+struct QuadRows {
+    char *row[4];  // this quad's rows (null: not stored), for piece `lane & 3`
+    __device__ __forceinline__ QuadRows(void *mine, bool real, int lane) {
+        const uint64_t p = real ? reinterpret_cast<uint64_t>(mine) : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint64_t q = __shfl_sync(0xffffffffu, p, (lane & ~3) + j);
+            row[j] = q ? reinterpret_cast<char *>(q) + (lane & 3) * 16 : nullptr;
+        }
+    }
+    // u: 64 bytes of the lane's own row, which start `offset` bytes into it
+    __device__ __forceinline__ void store(uint32_t (&u)[16], int offset, int lane) const {
+        const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+        for (int k = 0; k < 16; k += 8)  // pieces 0 <-> 1, 2 <-> 3 with the neighbour
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t r = __shfl_xor_sync(0xffffffffu, odd ? u[k + e] : u[k + 4 + e], 1);
+                (odd ? u[k + e] : u[k + 4 + e]) = r;
+            }
+#pragma unroll
+        for (int k = 0; k < 8; k += 4)  // pieces 0 <-> 2, 1 <-> 3 with the next pair
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t r = __shfl_xor_sync(0xffffffffu, high ? u[k + e] : u[k + 8 + e], 2);
+                (high ? u[k + e] : u[k + 8 + e]) = r;
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (row[j]) *reinterpret_cast<uint4 *>(row[j] + offset) = make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+    }
+    __device__ __forceinline__ void store_bf16(const float (&y)[32], float f, int offset, int lane) const {
+        uint32_t u[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] = bf16_pair(y[2 * i] * f, y[2 * i + 1] * f);
+        store(u, offset, lane);
+    }
+    __device__ __forceinline__ void store_f32(const float (&y)[32], int offset, int lane) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(y[16 * h + i]);
+            store(u, offset + 64 * h, lane);
+        }
+    }
+};
+
 // One lane of a converged warp, always the same.  The compiler knows that a branch on
 // it holds a single thread and keeps the operands of tcgen05.mma in uniform registers.
 __device__ __forceinline__ bool elect_one() {

@@ -78,37 +78,25 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {  // eight bf16 product
     };
     return (two(a.x, b.x) + two(a.y, b.y)) + (two(a.z, b.z) + two(a.w, b.w));
 }
-// one row of a [128 x d] accumulator, scaled, to global memory
-template <int D> __device__ __forceinline__ void store_row(uint32_t t, float f, __nv_bfloat16 *dst, bool real) {
+// one row of a [128 x d] accumulator per lane, scaled, to global memory (as bf16; or fp32 as it is)
+template <int D> __device__ __forceinline__ void store_row(uint32_t t, float f, __nv_bfloat16 *dst, bool real, int lane) {
+    const QuadRows out(dst, real, lane);
 #pragma unroll
     for (int h = 0; h < D / 32; ++h) {
         float y[32];
         tmem_ld32(t + h * 32, y);
         wait_loads(y);
-        if (real) {
-            uint4 *p = reinterpret_cast<uint4 *>(dst + h * 32);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                p[i] = make_uint4(bf16_pair(y[8 * i] * f, y[8 * i + 1] * f), bf16_pair(y[8 * i + 2] * f, y[8 * i + 3] * f),
-                                  bf16_pair(y[8 * i + 4] * f, y[8 * i + 5] * f), bf16_pair(y[8 * i + 6] * f, y[8 * i + 7] * f));
-        }
-        __syncwarp();
+        out.store_bf16(y, f, h * 64, lane);
     }
 }
-
-// the same in fp32, unscaled
-template <int D> __device__ __forceinline__ void store_part(uint32_t t, float *dst, bool real) {
+template <int D> __device__ __forceinline__ void store_part(uint32_t t, float *dst, bool real, int lane) {
+    const QuadRows out(dst, real, lane);
 #pragma unroll
     for (int h = 0; h < D / 32; ++h) {
         float y[32];
         tmem_ld32(t + h * 32, y);
         wait_loads(y);
-        if (real) {
-            float4 *p = reinterpret_cast<float4 *>(dst + h * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-        }
-        __syncwarp();
+        out.store_f32(y, h * 128, lane);
     }
 }
 
@@ -397,13 +385,13 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             ++na;
             tc_fence_after();
             if (t.slot >= 0) {  // one of several pieces of this tile's rows
-                store_part<D>((w ? t_dk : t_dv) + lanes, b.part + (((int64_t)t.slot * 2 + w) * 128 + key) * D, key < t.nkeys);
+                store_part<D>((w ? t_dk : t_dv) + lanes, b.part + (((int64_t)t.slot * 2 + w) * 128 + key) * D, key < t.nkeys, lane);
                 tc_fence_before();
                 continue;
             }
             const int64_t at = (int64_t)t.plane * a.plane[0] + (int64_t)(t.key0 + key) * D;
-            if (w == 0) store_row<D>(t_dv + lanes, 1.f, static_cast<__nv_bfloat16 *>(b.dv) + at, key < t.nkeys);
-            else store_row<D>(t_dk + lanes, a.scale, static_cast<__nv_bfloat16 *>(b.dk) + at, key < t.nkeys);
+            if (w == 0) store_row<D>(t_dv + lanes, 1.f, static_cast<__nv_bfloat16 *>(b.dv) + at, key < t.nkeys, lane);
+            else store_row<D>(t_dk + lanes, a.scale, static_cast<__nv_bfloat16 *>(b.dk) + at, key < t.nkeys, lane);
             tc_fence_before();
         }
     }
@@ -702,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
             ++na;
             tc_fence_after();
             // each warpgroup stores half of the row
-            store_row<D / 2>(t_dq + lanes + w * (D / 2), a.scale, static_cast<__nv_bfloat16 *>(b.dq) + row * D + w * (D / 2), real);
+            store_row<D / 2>(t_dq + lanes + w * (D / 2), a.scale, static_cast<__nv_bfloat16 *>(b.dq) + row * D + w * (D / 2), real, lane);
             tc_fence_before();
         }
     }

@@ -533,6 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                 if (a.decode) a.plse[prow] = lse;
                 else if (a.lse) a.lse[row] = lse;
             }
+            const QuadRows out(a.decode ? static_cast<void *>(a.po + prow * D) : static_cast<__nv_bfloat16 *>(a.o) + row * D,
+                               warp_rows && real, lane);
 #pragma unroll
             for (int h = 0; h < D / 32; ++h) {
                 if (!warp_rows) break;
@@ -548,17 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
 #pragma unroll
                     for (int i = 0; i < 32; ++i) y[i] += y1[i] * inv1;
                 }
-                if (real && a.decode) {
-                    float4 *p = reinterpret_cast<float4 *>(a.po + prow * D + h * 32);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) p[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-                } else if (real) {
-                    uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row * D + h * 32);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        p[i] = make_uint4(bf16_pair(y[8 * i], y[8 * i + 1]), bf16_pair(y[8 * i + 2], y[8 * i + 3]),
-                                          bf16_pair(y[8 * i + 4], y[8 * i + 5]), bf16_pair(y[8 * i + 6], y[8 * i + 7]));
-                }
+                if (a.decode) out.store_f32(y, h * 128, lane);
+                else out.store_bf16(y, 1.f, h * 64, lane);
                 __syncwarp();
             }
             tc_fence_before();
