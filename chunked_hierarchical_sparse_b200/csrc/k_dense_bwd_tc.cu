@@ -81,7 +81,7 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {  // eight bf16 product
 // one row of a [128 x d] accumulator per lane, scaled, to global memory (as bf16; or fp32 as it is)
 template <int D> __device__ __forceinline__ void store_row(uint32_t t, float f, __nv_bfloat16 *dst, bool real, int lane) {
     const QuadRows out(dst, real, lane);
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < D / 32; ++h) {
         float y[32];
         tmem_ld32(t + h * 32, y);
@@ -91,7 +91,7 @@ template <int D> __device__ __forceinline__ void store_row(uint32_t t, float f, 
 }
 template <int D> __device__ __forceinline__ void store_part(uint32_t t, float *dst, bool real, int lane) {
     const QuadRows out(dst, real, lane);
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < D / 32; ++h) {
         float y[32];
         tmem_ld32(t + h * 32, y);

@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                         l *= f;
                         if (j == 0) continue;
                         // S(j) is complete, so P.V(j-1) issued before it is, too
-#pragma unroll
+#pragma unroll 1
                         for (int h = 0; h < D / 16; ++h) rescale16(to + h * 16, f);
                         tmem_wait_st();
                     }
@@ -535,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             }
             const QuadRows out(a.decode ? static_cast<void *>(a.po + prow * D) : static_cast<__nv_bfloat16 *>(a.o) + row * D,
                                warp_rows && real, lane);
-#pragma unroll
+            // rolled: this code runs once per item and would be fetched anew each time
+#pragma unroll 1
             for (int h = 0; h < D / 32; ++h) {
                 if (!warp_rows) break;
                 float y[32];
