@@ -108,7 +108,9 @@ __device__ __forceinline__ void rescale16(uint32_t t, float f) {
         : "memory");
 }
 
-template <int D>
+// DECODE: the prefix part of a decode step (fp32 partials), else the prompt pass; two kernels,
+// since what an item runs once should be as little code as possible (instruction fetch).
+template <int D, bool DECODE>
 __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
     const __grid_constant__ CUtensorMap tm_v,
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             }
             const bool real = r < ntok * a.G;
             const int64_t row = ((int64_t)tok + rt) * a.hq + g * a.G + rh;
-            if (!a.decode && a.off_by_one) {  // the added 1 is a logit of 0
+            if (!DECODE && a.off_by_one) {  // the added 1 is a logit of 0
                 const float top = fmaxf(mm, 0.f), e = ex2(mm - top);
                 f *= e;
                 f1 *= e;
@@ -527,13 +529,13 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                 mm = top;
             }
             const float inv = z > 0.f ? f / z : (z == 0.f ? 0.f : z), inv1 = merge && z > 0.f ? f1 / z : 0.f;  // NaN stays NaN
-            const float lse = (mm + log2f(z)) * kLn2;
+            const float lse = (mm + lg2(z)) * kLn2;
             const int64_t prow = (int64_t)slot * a.B * a.hq + row;
             if (warp_rows && real) {
-                if (a.decode) a.plse[prow] = lse;
+                if (DECODE) a.plse[prow] = lse;
                 else if (a.lse) a.lse[row] = lse;
             }
-            const QuadRows out(a.decode ? static_cast<void *>(a.po + prow * D) : static_cast<__nv_bfloat16 *>(a.o) + row * D,
+            const QuadRows out(DECODE ? static_cast<void *>(a.po + prow * D) : static_cast<__nv_bfloat16 *>(a.o) + row * D,
                                warp_rows && real, lane);
             // rolled: this code runs once per item and would be fetched anew each time
 #pragma unroll 1
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
 #pragma unroll
                     for (int i = 0; i < 32; ++i) y[i] += y1[i] * inv1;
                 }
-                if (a.decode) out.store_f32(y, h * 128, lane);
+                if constexpr (DECODE) out.store_f32(y, h * 128, lane);
                 else out.store_bf16(y, 1.f, h * 64, lane);
                 __syncwarp();
             }
@@ -568,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
     if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
-template <int D>
+template <int D, bool DECODE>
 cudaError_t launch(const Args &a, int64_t items, int32_t *next, cudaStream_t st) {
     CUtensorMap mq, mk, mv;
     const uint64_t rows = (uint64_t)a.B * (a.decode ? 1 : a.L), planes = (uint64_t)a.hkv * (a.decode ? 1 : a.B);
@@ -577,12 +579,12 @@ cudaError_t launch(const Args &a, int64_t items, int32_t *next, cudaStream_t st)
         !make_map3(&mv, a.v[0], D, a.L, D, planes, a.plane[0], kKeys, 1))
         return cudaErrorInvalidValue;
     const size_t smem = Smem<D>::ALLOC;
-    cudaError_t e = set_smem_once((const void *)fwd_tc_kernel<D>, smem);
+    cudaError_t e = set_smem_once((const void *)fwd_tc_kernel<D, DECODE>, smem);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::min<int64_t>(items, sm_count());
     if (!a.plan && items <= grid) next = nullptr;
     else if (!a.plan && (e = cudaMemsetAsync(a.ds, 0, kWsHeader, st)) != cudaSuccess) return e;
-    return launch_next(a.plan != nullptr, fwd_tc_kernel<D>, grid, kThreads, smem, st, 1, mq, mk, mv, a, next,
+    return launch_next(a.plan != nullptr, fwd_tc_kernel<D, DECODE>, grid, kThreads, smem, st, 1, mq, mk, mv, a, next,
                        wait_limit_ns());
 }
 
@@ -629,7 +631,8 @@ bool make_map3(CUtensorMap *m, const void *base, uint64_t cols, uint64_t n1, uin
 }
 
 cudaError_t launch_fwd_tc(const Args &a, int d, int64_t items, int32_t *next, cudaStream_t st) {
-    return d == 128 ? launch<128>(a, items, next, st) : launch<64>(a, items, next, st);
+    if (a.decode) return d == 128 ? launch<128, true>(a, items, next, st) : launch<64, true>(a, items, next, st);
+    return d == 128 ? launch<128, false>(a, items, next, st) : launch<64, false>(a, items, next, st);
 }
 
 }  // namespace dense
