@@ -439,3 +439,103 @@ def test_prefill_then_decode(dtype):
     ref = {k_: oracle[k_][0, P:] for k_ in ("o", "o_b", "lse", "lse_b")}
     dt.check(f64(od), ref, "o", dtype)
     dt.check(f64(ld), ref, "lse", dtype)
+
+
+# ------------------------------------------------------------- calls side by side
+def test_two_streams_at_once():
+    """Prompt passes and decode steps issued on two streams without waiting in between."""
+    m = hsa()
+    xs = [inputs(1, 900 + 100 * i, 16, 2, 128, "bf16", seed=30 + i) for i in range(2)]
+    ds = [decode_inputs(9, 700 + i, 150, 16, 2, 128, "bf16", [150, 0, 3, 149, 64, 65, 1, 2, 150], seed=32 + i) for i in range(2)]
+    want = [run_prompt(x) for x in xs]
+    wantd = [run_decode(d) for d in ds]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, st in enumerate(streams):
+            x, d = xs[i], ds[i]
+            o, lse = m.hsa_prompt_fwd(x["q"], x["k"], x["v"], stream=st)
+            g = m.hsa_prompt_bwd(x["q"], x["k"], x["v"], o, x["dO"], lse, stream=st)
+            od, _ = m.hsa_prefix_decode(d["q"], d["kp"], d["vp"], d["kc"], d["vc"], d["lens"], stream=st)
+            got[i].append((o, *g, od))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, dq, dk, dv, od in got[i]:
+            w = want[i]
+            assert all(torch.equal(a, w[n]) for a, n in ((o, "o"), (dq, "dq"), (dk, "dk"), (dv, "dv")))
+            assert torch.equal(od, wantd[i]["o"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_one_workspace_for_calls_of_different_sizes(dtype):
+    """What a call left in the workspace does not matter to the next."""
+    m = hsa()
+    ws = torch.empty(1 << 27, dtype=torch.uint8, device=DEV)
+    for L, G, seed in ((700, 8, 40), (33, 3, 41), (512, 1, 42)):
+        x = inputs(1, L, 2 * G, 2, 64, dtype, seed=seed)
+        cu = cu_of([L // 3, 0, L - L // 3])
+        want = run_prompt(x, cu)
+        ws.random_(0, 255)
+        o, lse = m.hsa_prompt_fwd(x["q"], x["k"], x["v"], cu, ws=ws)
+        ws.random_(0, 255)
+        g = m.hsa_prompt_bwd(x["q"], x["k"], x["v"], o, x["dO"], lse, cu, ws=ws)
+        assert torch.equal(o, want["o"]) and all(torch.equal(a, want[n]) for a, n in zip(g, ("dq", "dk", "dv")))
+        d = decode_inputs(5, L, 40, 2 * G, 2, 64, dtype, [40, 1, 0, 39, 7], seed=seed)
+        wd = run_decode(d)
+        ws.random_(0, 255)
+        assert torch.equal(m.hsa_prefix_decode(d["q"], d["kp"], d["vp"], d["kc"], d["vc"], d["lens"], ws=ws)[0], wd["o"])
+
+
+@pytest.mark.parametrize("L,n_seq", [(3000, 1), (5000, 3), (2600, 40)])
+def test_prompt_long_and_packed_cut(L, n_seq):
+    """Sizes at which streams split the keys and key tiles are cut into pieces, against fp64 on the GPU
+    for one head and, for the rest, against the same prompts computed one at a time."""
+    rng = np.random.default_rng(L)
+    ends = np.sort(rng.integers(0, L + 1, n_seq - 1))
+    lens = np.diff(np.concatenate([[0], ends, [L]]))
+    x = inputs(1, L, 10, 2, 128, "bf16", seed=L)
+    cu = cu_of(lens)
+    b = run_prompt(x, cu, True)
+    for _, t, n in spans_of(cu):
+        if n == 0:
+            continue
+        ts = slice(t, t + n)
+        one = {nm: x[nm][:, ts].contiguous() for nm in ("q", "dO")} | {nm: x[nm][:, :, ts].contiguous() for nm in ("k", "v")}
+        r = run_prompt(one, None, True)
+        # the same sums in another grouping: fp32 sums of bf16 products, so a rounding of the output
+        # (2^-8 of it, both sides) and of the operands p and dS (2^-8 of a sum's terms each side)
+        for nm, sl in (("o", np.s_[:, ts]), ("dq", np.s_[:, ts]), ("dk", np.s_[:, :, ts]), ("dv", np.s_[:, :, ts])):
+            u, w = b[nm][sl].double(), r[nm].double()
+            assert float((u - w).norm() / w.norm()) <= 2 ** -8, nm
+    q, k, v, dO = (x[nm].double() for nm in ("q", "k", "v", "dO"))
+    h, g = 7, 1  # one head of the second group
+    o = torch.zeros(L, 128, dtype=torch.float64, device=DEV)
+    dq = torch.zeros_like(o)
+    for _, t, n in spans_of(cu):
+        ts = slice(t, t + n)
+        s = (q[0, ts, h] @ k[0, g, ts].T) / 128 ** 0.5
+        s.masked_fill_(torch.ones_like(s, dtype=torch.bool).triu(1), -np.inf)
+        p = torch.exp(s) / (1 + torch.exp(s).sum(1, keepdim=True))
+        o[ts] = p @ v[0, g, ts]
+        dp = dO[0, ts, h] @ v[0, g, ts].T
+        dq[ts] = (p * (dp - (dO[0, ts, h] * o[ts]).sum(1, keepdim=True))) @ k[0, g, ts] / 128 ** 0.5
+    # relative 2-norms: p and the output are rounded (2^-9 rms at most each): 2^-8; dS, dq and D: 2^-7
+    assert float((b["o"][0, :, h].double() - o).norm() / o.norm()) <= 2 ** -8
+    assert float((b["dq"][0, :, h].double() - dq).norm() / dq.norm()) <= 2 ** -7
+
+
+def test_prompt_strided_views_are_refused():
+    m = hsa()
+    x = inputs(1, 64, 8, 2, 64, "bf16")
+    with pytest.raises(ValueError):
+        m.hsa_prompt_fwd(x["q"].transpose(1, 2), x["k"], x["v"])
+    with pytest.raises(ValueError):
+        m.hsa_prompt_fwd(x["q"], x["k"].transpose(2, 3).contiguous().transpose(2, 3), x["v"])
+    d = decode_inputs(2, 64, 8, 8, 2, 64, "bf16", [8, 8])
+    with pytest.raises(m.HsaError):  # planes that overlap
+        m.hsa_prefix_decode(d["q"], d["kp"][:1].expand(2, -1, -1), d["vp"][:1].expand(2, -1, -1), d["kc"], d["vc"], d["lens"])
+    with pytest.raises(ValueError):
+        m.hsa_prefix_decode(d["q"], d["kp"][:, ::2], d["vp"][:, ::2], d["kc"], d["vc"], d["lens"])
+    with pytest.raises(TypeError):
+        m.hsa_prefix_decode(d["q"], d["kp"], d["vp"], d["kc"], d["vc"], d["lens"].long())
