@@ -45,14 +45,14 @@ constexpr int kSweep = 2;   // row pass: rows of at most so many key tiles take 
 template <int D, bool KEYS> struct Smem {
     static constexpr int NH = D / 64;
     static constexpr int TILE = NH * 128 * 128;           // bytes of a 128 x D bf16 tile
-    static constexpr int ST = KEYS ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);
+    static constexpr int ST = D == 128 ? 5 : 10;
     static constexpr int OFF_FIX = 0;                     // the two stationary tiles
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int OFF_STAT = OFF_RING + ST * TILE; // key pass: [2][lse, delta][128]; row pass: [2][128]
     static constexpr int OFF_ITEM = OFF_STAT + (KEYS ? 2048 : 1024);
     static constexpr int OFF_BAR = OFF_ITEM + kItems * 64;
-    static constexpr int OFF_MISC = OFF_BAR + 512;
-    static constexpr int ALLOC = OFF_MISC + 64 + 1024;    // + alignment to 1 KB
+    static constexpr int OFF_MISC = OFF_BAR + 320;
+    static constexpr int ALLOC = OFF_MISC + 64;
 };
 static_assert(Smem<128, true>::ALLOC <= 232448 && Smem<128, false>::ALLOC <= 232448, "shared memory of a CTA");
 
@@ -119,8 +119,11 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     const __grid_constant__ BwdArgs b, int32_t *next, uint64_t wait_ns) {
     using L = Smem<D, true>;
     const Args &a = b.a;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];  // (no room to align it by hand)
+    if (smem_u32(sm) & 1023) {
+        if (threadIdx.x == 0) report(a.ds, HSA_ERR_CUDA, kKDense, 1024, 0);
+        return;
+    }
     float *stat = reinterpret_cast<float *>(sm + L::OFF_STAT);
     BwdItem *items = reinterpret_cast<BwdItem *>(sm + L::OFF_ITEM);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
@@ -260,27 +263,29 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                 mma_commit(dp_full);
                 for (int j = j0; j < j1; ++j) {
                     const bool more = j + 1 < j1;
-                    if (more && !(ok = take(j + 1, qn))) break;
                     if (!(ok = wait1(p_full, np))) break;
                     tc_fence_after();
                     mma_sum<D, 64>(t_dv, t_s, tile(d), j > j0);
+                    mma_commit(&ring_empty[d.st]);
                     if (more) {
+                        if (!(ok = take(j + 1, qn))) break;
+                        tc_fence_after();
                         mma_dots<D>(t_s, kb, tile(qn));
                         mma_commit(s_full);
                     }
-                    mma_commit(&ring_empty[d.st]);
-                    if (more && !(ok = take(j + 1, d))) break;
                     if (!(ok = wait1(ds_full, np++))) break;
                     tc_fence_after();
                     mma_sum<D, 64>(t_dk, t_dp, tile(q), j > j0);
+                    mma_commit(&ring_empty[q.st]);
                     if (more) {
+                        if (!(ok = take(j + 1, d))) break;
+                        tc_fence_after();
                         mma_dots<D>(t_dp, vb, tile(d));
                         mma_commit(dp_full);
                     } else {
                         mma_commit(acc_full);
                         mma_commit(fix_empty);
                     }
-                    mma_commit(&ring_empty[q.st]);
                     q = qn;
                 }
             }
@@ -409,8 +414,11 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     const __grid_constant__ BwdArgs b, int32_t *next, uint64_t wait_ns) {
     using L = Smem<D, false>;
     const Args &a = b.a;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];  // (no room to align it by hand)
+    if (smem_u32(sm) & 1023) {
+        if (threadIdx.x == 0) report(a.ds, HSA_ERR_CUDA, kKDense, 1024, 0);
+        return;
+    }
     float *joint = reinterpret_cast<float *>(sm + L::OFF_STAT);  // [2][128]
     BwdItem *items = reinterpret_cast<BwdItem *>(sm + L::OFF_ITEM);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
