@@ -113,6 +113,14 @@ __device__ __forceinline__ void wait_loads(float (&x)[32]) {
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 // Rows that the lanes of a warp hold one each (64 bytes at a time) go to global memory in
 // pieces of 16 bytes that the four lanes of a quad first exchange, so that a store writes
 // 64 consecutive bytes of 8 rows instead of 16 bytes of 32: the load/store unit takes a

@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __grid_constant__ BwdArgs b, int32_t *next, uint64_t wait_ns) {
     using L = Smem<D, true>;
+    constexpr bool kHalves = D == 128;  // P is handed over in halves (d = 64: the products are too short for it)
     const Args &a = b.a;
     extern __shared__ __align__(1024) uint8_t sm[];  // (no room to align it by hand)
     if (smem_u32(sm) & 1023) {
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     uint64_t *item_full = bar, *item_empty = bar + 2, *fix_full = bar + 4, *fix_empty = bar + 5;
     uint64_t *stat_full = bar + 6, *stat_empty = bar + 8;
     uint64_t *s_full = bar + 10, *dp_full = bar + 11, *p_full = bar + 12, *ds_full = bar + 13, *acc_full = bar + 14;
-    uint64_t *done = bar + 15, *clean = bar + 16, *clear_req = bar + 17, *ring_full = bar + 18, *ring_empty = ring_full + L::ST;
+    uint64_t *done = bar + 15, *clean = bar + 16, *clear_req = bar + 17, *p_half = bar + 18, *ring_full = bar + 19, *ring_empty = ring_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
     volatile int *clear_job = abort_flag + 1;  // stage, first row
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             mbar_init(&stat_full[i], 1); mbar_init(&stat_empty[i], 8);
         }
         mbar_init(fix_full, 1); mbar_init(fix_empty, 1);
-        mbar_init(s_full, 1); mbar_init(dp_full, 1); mbar_init(p_full, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
+        mbar_init(s_full, 1); mbar_init(dp_full, 1); mbar_init(p_half, 8); mbar_init(p_full, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
         mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
         *abort_flag = 0;
@@ -263,9 +264,20 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                 mma_commit(dp_full);
                 for (int j = j0; j < j1; ++j) {
                     const bool more = j + 1 < j1;
+                    if constexpr (kHalves) {
+                        if (!(ok = wait1(p_half, np))) break;
+                        tc_fence_after();
+                        mma_sum<D, 64, 0, 2>(t_dv, t_s, tile(d), j > j0);
+                        mma_sum<D, 64, 4, 6>(t_dv, t_s, tile(d), 1);
+                    }
                     if (!(ok = wait1(p_full, np))) break;
                     tc_fence_after();
-                    mma_sum<D, 64>(t_dv, t_s, tile(d), j > j0);
+                    if constexpr (kHalves) {
+                        mma_sum<D, 64, 2, 4>(t_dv, t_s, tile(d), 1);
+                        mma_sum<D, 64, 6, 8>(t_dv, t_s, tile(d), 1);
+                    } else {
+                        mma_sum<D, 64>(t_dv, t_s, tile(d), j > j0);
+                    }
                     mma_commit(&ring_empty[d.st]);
                     if (more) {
                         if (!(ok = take(j + 1, qn))) break;
@@ -353,22 +365,31 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                 float x[64];
                 load64(xs, x);
                 const float2 c2 = make_float2(c, c);
+                const bool edge = j * tt < t.off + kTile - 1;  // some row of the tile does not see some of the keys
+                const int first = (t.off + key - j * tt) * a.G - w * 64;  // first column that sees this key
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float4 l = s4[i];
-                    const float2 u = fma2(make_float2(x[4 * i], x[4 * i + 1]), c2, make_float2(-l.x, -l.y));
-                    const float2 v = fma2(make_float2(x[4 * i + 2], x[4 * i + 3]), c2, make_float2(-l.z, -l.w));
-                    x[4 * i] = ex2(u.x); x[4 * i + 1] = ex2(u.y); x[4 * i + 2] = ex2(v.x); x[4 * i + 3] = ex2(v.y);
-                }
-                if (j * tt < t.off + kTile - 1) {  // some row of the tile does not see some of the keys
-                    const int first = (t.off + key - j * tt) * a.G - w * 64;  // first column that sees this key
+                for (int h = 0; h < 2; ++h) {  // the first half is multiplied while the second is exponentials
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) x[i] = i >= first ? x[i] : 0.f;
+                    for (int i = 8 * h; i < 8 * h + 8; ++i) {
+                        const float4 l = s4[i];
+                        const float2 u = fma2(make_float2(x[4 * i], x[4 * i + 1]), c2, make_float2(-l.x, -l.y));
+                        const float2 v = fma2(make_float2(x[4 * i + 2], x[4 * i + 3]), c2, make_float2(-l.z, -l.w));
+                        x[4 * i] = ex2(u.x); x[4 * i + 1] = ex2(u.y); x[4 * i + 2] = ex2(v.x); x[4 * i + 3] = ex2(v.y);
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int i = 32 * h; i < 32 * h + 32; ++i) x[i] = i >= first ? x[i] : 0.f;
+                    }
+                    uint32_t u[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) u[i] = bf16_pair(x[32 * h + 2 * i], x[32 * h + 2 * i + 1]);
+                    tmem_st16(xs + 16 * h, u);
+                    if (!h && !kHalves) continue;
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_lane0(h ? p_full : p_half, lane);
                 }
-                store64(xs, x);
-                tc_fence_before();
-                __syncwarp();
-                mbar_arrive_lane0(p_full, lane);
                 if (!(ok = wait(dp_full, nt, 14))) break;
                 tc_fence_after();
                 float y[64];
