@@ -40,6 +40,7 @@ constexpr int kThreads = 384;
 constexpr int kTile = 128;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpStat = 10, kWarpClear = 11;
 constexpr int kItems = 2;
+constexpr int kBarriers = 22;    // besides the ring's
 constexpr int kSweep = 2;   // row pass: rows of at most so many key tiles take D from a sweep of their own
 
 template <int D, bool KEYS> struct Smem {
@@ -51,8 +52,9 @@ template <int D, bool KEYS> struct Smem {
     static constexpr int OFF_STAT = OFF_RING + ST * TILE; // key pass: [2][lse, delta][128]; row pass: [2][128]
     static constexpr int OFF_ITEM = OFF_STAT + (KEYS ? 2048 : 1024);
     static constexpr int OFF_BAR = OFF_ITEM + kItems * 64;
-    static constexpr int OFF_MISC = OFF_BAR + 320;
+    static constexpr int OFF_MISC = OFF_BAR + 384;
     static constexpr int ALLOC = OFF_MISC + 64;
+    static_assert((kBarriers + 2 * ST) * 8 <= 384, "barriers");
 };
 static_assert(Smem<128, true>::ALLOC <= 232448 && Smem<128, false>::ALLOC <= 232448, "shared memory of a CTA");
 
@@ -118,7 +120,10 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __grid_constant__ BwdArgs b, int32_t *next, uint64_t wait_ns) {
     using L = Smem<D, true>;
-    constexpr bool kHalves = D == 128;  // P is handed over in halves (d = 64: the products are too short for it)
+    // d = 128: dV, dK, dP and one S fill tensor memory; P is handed over in halves, so that its first
+    // product runs under the second half's exponentials.  d = 64: a second S fits, so the next S is
+    // computed ahead of the P that the first holds.
+    constexpr bool kTwoS = D == 64, kHalves = !kTwoS;
     const Args &a = b.a;
     extern __shared__ __align__(1024) uint8_t sm[];  // (no room to align it by hand)
     if (smem_u32(sm) & 1023) {
@@ -130,8 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
     uint64_t *item_full = bar, *item_empty = bar + 2, *fix_full = bar + 4, *fix_empty = bar + 5;
     uint64_t *stat_full = bar + 6, *stat_empty = bar + 8;
-    uint64_t *s_full = bar + 10, *dp_full = bar + 11, *p_full = bar + 12, *ds_full = bar + 13, *acc_full = bar + 14;
-    uint64_t *done = bar + 15, *clean = bar + 16, *clear_req = bar + 17, *p_half = bar + 18, *ring_full = bar + 19, *ring_empty = ring_full + L::ST;
+    uint64_t *s_full = bar + 20, *dp_full = bar + 11, *p_full = bar + 12, *ds_full = bar + 13, *acc_full = bar + 14;
+    uint64_t *done = bar + 15, *clean = bar + 16, *clear_req = bar + 17, *p_half = bar + 18, *ring_full = bar + kBarriers, *ring_empty = ring_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
     volatile int *clear_job = abort_flag + 1;  // stage, first row
@@ -144,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             mbar_init(&stat_full[i], 1); mbar_init(&stat_empty[i], 8);
         }
         mbar_init(fix_full, 1); mbar_init(fix_empty, 1);
-        mbar_init(s_full, 1); mbar_init(dp_full, 1); mbar_init(p_half, 8); mbar_init(p_full, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
+        mbar_init(s_full, 1); mbar_init(s_full + 1, 1); mbar_init(dp_full, 1); mbar_init(p_half, 8); mbar_init(p_full, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
         mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
         *abort_flag = 0;
@@ -169,7 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     const uint32_t tmem = uniform(*tmem_slot);
     dependency_wait();
     dependents_may_start();
-    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + D;
+    const uint32_t t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + D;
+    auto t_s = [&](int step) { return tmem + (kTwoS && (step & 1) ? 384u : 0u); };
     auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
     if (warp == kWarpLoad) {
         // ============================================================ items and loads
@@ -257,34 +263,39 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                 Ring<L::ST> q, d, qn;
                 if (!(ok = wait1(fix_full, n) && take(j0, q))) break;
                 tc_fence_after();
-                mma_dots<D>(t_s, kb, tile(q));
-                mma_commit(s_full);
+                auto s_done = [&](int step) { return &s_full[kTwoS ? step & 1 : 0]; };
+                mma_dots<D>(t_s(np), kb, tile(q));
+                mma_commit(s_done(np));
                 if (!(ok = take(j0, d))) break;
                 mma_dots<D>(t_dp, vb, tile(d));
                 mma_commit(dp_full);
                 for (int j = j0; j < j1; ++j) {
                     const bool more = j + 1 < j1;
-                    if constexpr (kHalves) {
+                    auto next_scores = [&]() -> bool {
+                        if (!take(j + 1, qn)) return false;
+                        tc_fence_after();
+                        mma_dots<D>(t_s(np + 1), kb, tile(qn));
+                        mma_commit(s_done(np + 1));
+                        return true;
+                    };
+                    if constexpr (kTwoS) {  // (the loads' order: this tile's dO was taken with its dP)
+                        if (more && !(ok = next_scores())) break;
+                    } else {
                         if (!(ok = wait1(p_half, np))) break;
                         tc_fence_after();
-                        mma_sum<D, 64, 0, 2>(t_dv, t_s, tile(d), j > j0);
-                        mma_sum<D, 64, 4, 6>(t_dv, t_s, tile(d), 1);
+                        mma_sum<D, 64, 0, 2>(t_dv, t_s(np), tile(d), j > j0);
+                        mma_sum<D, 64, 4, 6>(t_dv, t_s(np), tile(d), 1);
                     }
                     if (!(ok = wait1(p_full, np))) break;
                     tc_fence_after();
-                    if constexpr (kHalves) {
-                        mma_sum<D, 64, 2, 4>(t_dv, t_s, tile(d), 1);
-                        mma_sum<D, 64, 6, 8>(t_dv, t_s, tile(d), 1);
+                    if constexpr (kTwoS) {
+                        mma_sum<D, 64>(t_dv, t_s(np), tile(d), j > j0);
                     } else {
-                        mma_sum<D, 64>(t_dv, t_s, tile(d), j > j0);
+                        mma_sum<D, 64, 2, 4>(t_dv, t_s(np), tile(d), 1);
+                        mma_sum<D, 64, 6, 8>(t_dv, t_s(np), tile(d), 1);
                     }
                     mma_commit(&ring_empty[d.st]);
-                    if (more) {
-                        if (!(ok = take(j + 1, qn))) break;
-                        tc_fence_after();
-                        mma_dots<D>(t_s, kb, tile(qn));
-                        mma_commit(s_full);
-                    }
+                    if (!kTwoS && more && !(ok = next_scores())) break;
                     if (!(ok = wait1(ds_full, np++))) break;
                     tc_fence_after();
                     mma_sum<D, 64>(t_dk, t_dp, tile(q), j > j0);
@@ -346,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
         // ============================================================ p and dS, 64 columns per warpgroup
         const int w = warp >> 2, key = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t xs = t_s + lanes + w * 64, xd = t_dp + lanes + w * 64;
+        const uint32_t xd = t_dp + lanes + w * 64;
         const float c = a.scale_log2;
         int nt = 0, na = 0;
         bool ok = true;
@@ -360,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             for (int j = t.j0; j < t.j1; ++j, ++nt) {
                 const float4 *s4 = reinterpret_cast<const float4 *>(stat + (nt & 1) * 256 + w * 64);
                 if (!(ok = wait(&stat_full[nt & 1], nt >> 1, 14))) break;
-                if (!(ok = wait(s_full, nt, 14))) break;
+                const uint32_t xs = t_s(nt) + lanes + w * 64;
+                if (!(ok = wait(kTwoS ? &s_full[nt & 1] : s_full, kTwoS ? nt >> 1 : nt, 14))) break;
                 tc_fence_after();
                 float x[64];
                 load64(xs, x);
@@ -445,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
     uint64_t *item_full = bar, *item_empty = bar + 2, *fix_full = bar + 4, *fix_empty = bar + 5;
     uint64_t *s_full = bar + 6, *dp_full = bar + 8, *dp_read = bar + 9, *ds_full = bar + 10, *acc_full = bar + 11;
-    uint64_t *done = bar + 12, *clean = bar + 13, *clear_req = bar + 14, *join = bar + 15, *ring_full = bar + 16, *ring_empty = ring_full + L::ST;
+    uint64_t *done = bar + 12, *clean = bar + 13, *clear_req = bar + 14, *join = bar + 15, *ring_full = bar + kBarriers, *ring_empty = ring_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
     volatile int *clear_job = abort_flag + 1;  // stage, first row

@@ -51,6 +51,7 @@ template <int D> struct Smem {
     static constexpr int ALLOC = OFF_MISC + 64 + 1024;  // + alignment to 1 KB
 };
 static_assert(Smem<128>::ALLOC <= 232448 && Smem<64>::ALLOC <= 232448, "shared memory of a CTA");
+static_assert((2 * kItems + 17 + 2 * Smem<64>::ST) * 8 <= 512, "barriers");
 
 struct TcItem {
     int end, plane, g, shared, foreign, slot;
