@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
 // ---------------------------------------------------------------------- row pass
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
-    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
+    const __grid_constant__ CUtensorMap tm_do,
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __grid_constant__ BwdArgs b, int32_t *next, uint64_t wait_ns) {
     using L = Smem<D, false>;
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
     uint64_t *item_full = bar, *item_empty = bar + 2, *fix_full = bar + 4, *fix_empty = bar + 5;
     uint64_t *s_full = bar + 6, *dp_full = bar + 8, *dp_read = bar + 9, *ds_full = bar + 10, *acc_full = bar + 11;
-    uint64_t *done = bar + 12, *clean = bar + 13, *clear_req = bar + 14, *join = bar + 15, *ring_full = bar + kBarriers, *ring_empty = ring_full + L::ST;
+    uint64_t *done = bar + 12, *clean = bar + 13, *clear_req = bar + 14, *join = bar + 15, *out_read = bar + 16, *ring_full = bar + kBarriers, *ring_empty = ring_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
     volatile int *clear_job = abort_flag + 1;  // stage, first row
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
         for (int i = 0; i < 2; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 9); mbar_init(&s_full[i], 1); }
         mbar_init(fix_full, 1); mbar_init(fix_empty, 1);
         mbar_init(dp_full, 1); mbar_init(dp_read, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
-        mbar_init(join, 8);
+        mbar_init(join, 8); mbar_init(out_read, 8);
         mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
         *abort_flag = 0;
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
         tmem_relinquish();
     }
     if (warp == kWarpLoad && lane == 0) {
-        prefetch_tmap(&tm_q); prefetch_tmap(&tm_do); prefetch_tmap(&tm_k); prefetch_tmap(&tm_v);
+        prefetch_tmap(&tm_q); prefetch_tmap(&tm_o); prefetch_tmap(&tm_do); prefetch_tmap(&tm_k); prefetch_tmap(&tm_v);
     }
     tc_fence_before();
     __syncthreads();
@@ -513,7 +514,24 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
             }
             __syncwarp();
             if (t.end) break;
-            if (n > 0 && !(ok = wait(fix_empty, n - 1, 21))) break;
+            const int nt = tiles(t.nkeys), sw = sweep(nt), all = nt + sw;
+            auto load = [&](const CUtensorMap *m, int bytes, int y, int z) -> bool {
+                const int st = pos % L::ST;
+                if (pos >= L::ST && !wait(&ring_empty[st], pos / L::ST - 1, 21)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&ring_full[st], bytes);
+#pragma unroll
+                    for (int h = 0; h < L::NH; ++h)
+                        tma_load_3d(sm + L::OFF_RING + st * L::TILE + h * 16384, m, h * 64, y, z, &ring_full[st]);
+                }
+                ++pos;
+                return true;
+            };
+            // the ring's first tiles do not wait for the item before: rows without a sweep, their
+            // stored output (for D = dO . o); the first K and V
+            if (!sw) ok = load(&tm_o, L::NH * rows * 128, t.g * a.G, t.tok0);
+            ok = ok && load(&tm_k, L::TILE, t.key0, t.plane) && load(&tm_v, L::TILE, t.key0, t.plane);
+            if (!ok || (n > 0 && !(ok = wait(fix_empty, n - 1, 21)))) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(fix_full, 2 * L::NH * rows * 128);
 #pragma unroll
@@ -523,21 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                 }
             }
             ++fixes;
-            const int nt = tiles(t.nkeys), all = nt + sweep(nt);
-            for (int j = 0; ok && j < all; ++j) {
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    const int st = pos % L::ST;
-                    if (pos >= L::ST && !(ok = wait(&ring_empty[st], pos / L::ST - 1, 21))) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&ring_full[st], L::TILE);
-#pragma unroll
-                        for (int h = 0; h < L::NH; ++h)
-                            tma_load_3d(sm + L::OFF_RING + st * L::TILE + h * 16384, o ? &tm_v : &tm_k, h * 64,
-                                        t.key0 + (j < nt ? j : j - nt) * kTile, t.plane, &ring_full[st]);
-                    }
-                    ++pos;
-                }
+            for (int j = 1; ok && j < all; ++j) {
+                const int key = t.key0 + (j < sw ? j : j - sw) * kTile;
+                ok = load(&tm_k, L::TILE, key, t.plane) && load(&tm_v, L::TILE, key, t.plane);
             }
             int i = 0;
             if (lane == 0) i = atomicAdd(next, 1);
@@ -554,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
             auto wait1 = [&](uint64_t *x, uint32_t par) { return thread_wait(x, par & 1, wait_ns, abort_flag, a.ds, 22); };
             const uint32_t qb = smem_u32(sm + L::OFF_FIX), ob = qb + L::TILE;
             Ring<L::ST> ring;
-            int nt = 0, nc = 0, nd = 0;
+            int nt = 0, nc = 0, nd = 0, n_out = 0;
             bool ok = true;
             for (int n = 0; ok; ++n) {
                 const int ib = n % kItems;
@@ -594,7 +600,13 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                     return true;
                 };
                 Ring<L::ST> k, kn;
+                const Ring<L::ST> out = ring;
+                if (!sw) ring.next();
                 ok = scores(0, k) && dprob(0);
+                if (ok && !sw) {  // the warpgroups have read the output tile
+                    ok = wait1(out_read, n_out++);
+                    mbar_arrive(&ring_empty[out.st]);
+                }
                 for (int j = 0; ok && j < nn; ++j) {
                     // (S of step j + 1 goes over that of j - 1: read, and its dS multiplied, before dP of j)
                     if (j + 1 < nn) {
@@ -629,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
         const uint32_t xd = t_dp + lanes + w * 64;
         const float c = a.scale_log2;
         const int rt = r / a.G, rh = r % a.G;
-        int nt = 0, na = 0, n_join = 0;
+        int nt = 0, na = 0, n_join = 0, pos = 0;
         bool ok = true;
         for (int n = 0; ok; ++n) {
             const int ib = n % kItems;
@@ -645,12 +657,23 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
             const int lim = min(t.nkeys - 1, t.off + rt), lim_all = min(t.nkeys - 1, t.off);
             const int nk = tiles(t.nkeys), sw = sweep(nk);
             float dsum = 0.f;
-            if (!sw && real) {  // D = dO . o, half of the columns per warpgroup
-                const uint4 *po = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(b.o) + row * D + w * (D / 2));
-                const uint4 *pd = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(b.dO) + row * D + w * (D / 2));
+            if (!sw) {  // D = dO . o, half of the columns per warpgroup, from the tiles in shared memory
+                const int st = pos % L::ST;
+                if (!(ok = wait(fix_full, n, 24) && wait(&ring_full[st], pos / L::ST, 24))) break;
+                const int h = D == 128 ? w : 0, c0 = D == 128 ? 0 : 4 * w;  // 64-column half, first 16-byte piece
+                const uint8_t *po = sm + L::OFF_RING + st * L::TILE + h * 16384 + r * 128;
+                const uint8_t *pd = sm + L::OFF_FIX + L::TILE + h * 16384 + r * 128;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) dsum += dot8(po[i], pd[i]);
+                for (int i = 0; i < D / 16; ++i) {
+                    const int at = ((c0 + i) ^ (r & 7)) << 4;
+                    dsum += dot8(*reinterpret_cast<const uint4 *>(po + at), *reinterpret_cast<const uint4 *>(pd + at));
+                }
+                if (!real) dsum = 0.f;
+                ++pos;
+                __syncwarp();
+                mbar_arrive_lane0(out_read, lane);
             }
+            pos += 2 * (sw + nk);
             if (!sw) {
                 joint[w * 128 + r] = dsum;
                 __syncwarp();
@@ -744,10 +767,11 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
 template <int D>
 cudaError_t launch(const BwdArgs &b, int64_t row_items, int64_t key_items, int32_t *next, cudaStream_t st) {
     const Args &a = b.a;
-    CUtensorMap mq, mo, mk, mv;
+    CUtensorMap mq, mo, mg, mk, mv;
     const uint64_t toks = (uint64_t)a.B * a.L, tt = 128 / a.G, planes = (uint64_t)a.B * a.hkv;
     if (!make_map3(&mq, a.q, D, a.hq, D, toks, (uint64_t)a.hq * D, a.G, (uint32_t)tt) ||
-        !make_map3(&mo, b.dO, D, a.hq, D, toks, (uint64_t)a.hq * D, a.G, (uint32_t)tt) ||
+        !make_map3(&mo, b.o, D, a.hq, D, toks, (uint64_t)a.hq * D, a.G, (uint32_t)tt) ||
+        !make_map3(&mg, b.dO, D, a.hq, D, toks, (uint64_t)a.hq * D, a.G, (uint32_t)tt) ||
         !make_map3(&mk, a.k[0], D, a.L, D, planes, a.plane[0], kTile, 1) ||
         !make_map3(&mv, a.v[0], D, a.L, D, planes, a.plane[0], kTile, 1))
         return cudaErrorInvalidValue;
@@ -756,10 +780,10 @@ cudaError_t launch(const BwdArgs &b, int64_t row_items, int64_t key_items, int32
     if (e != cudaSuccess) return e;
     // the row pass first: it writes delta for the key pass
     e = launch_next(b.a.plan || b.kplan, bwd_row_tc_kernel<D>, (int)std::min<int64_t>(row_items, sm_count()), kThreads,
-                    Smem<D, false>::ALLOC, st, 1, mq, mo, mk, mv, b, next + 1, wait_limit_ns());
+                    Smem<D, false>::ALLOC, st, 1, mq, mo, mg, mk, mv, b, next + 1, wait_limit_ns());
     if (e != cudaSuccess) return e;
     return launch_next(true, bwd_key_tc_kernel<D>, (int)std::min<int64_t>(key_items, sm_count()), kThreads,
-                       Smem<D, true>::ALLOC, st, 1, mq, mo, mk, mv, b, next, wait_limit_ns());
+                       Smem<D, true>::ALLOC, st, 1, mq, mg, mk, mv, b, next, wait_limit_ns());
 }
 
 }  // namespace
