@@ -385,6 +385,8 @@ def _prompt_args(q, k, v, cu_seqlens, off_by_one):
     _need(v, "v", (B, h_kv, L, d), q.dtype, dev)
     n_seq = 0
     if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor):
+            raise TypeError("cu_seqlens must be a torch.Tensor")
         n_seq = cu_seqlens.numel() - 1
         if n_seq < 1 or B != 1:
             raise ValueError("cu_seqlens: at least two entries, with every sequence packed into one batch row (B = 1)")
@@ -485,7 +487,7 @@ def hsa_prefix_decode(q, k_prefix, v_prefix, k_cache, v_cache, lens, off_by_one:
     _need(v_cache, "v_cache", (B, h_kv, cap, d), q.dtype, dev)
     _need(lens, "lens", (B,), torch.int32, dev)
     stride = _prefix_planes(k_prefix, "k_prefix", h_kv, d, q.dtype, dev)
-    if v_prefix.shape != k_prefix.shape or _prefix_planes(v_prefix, "v_prefix", h_kv, d, q.dtype, dev) != stride:
+    if _prefix_planes(v_prefix, "v_prefix", h_kv, d, q.dtype, dev) != stride or v_prefix.shape != k_prefix.shape:
         raise ValueError("v_prefix must have k_prefix's shape and strides")
     sh, n = _prefix_shape(B, k_prefix.shape[1], cap, h_q, h_kv, d, 1 if off_by_one else 0, dt, stride)
     if n == 0:

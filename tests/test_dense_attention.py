@@ -539,3 +539,19 @@ def test_prompt_strided_views_are_refused():
         m.hsa_prefix_decode(d["q"], d["kp"][:, ::2], d["vp"][:, ::2], d["kc"], d["vc"], d["lens"])
     with pytest.raises(TypeError):
         m.hsa_prefix_decode(d["q"], d["kp"], d["vp"], d["kc"], d["vc"], d["lens"].long())
+
+
+def test_missing_tensors_are_refused():
+    m = hsa()
+    x = inputs(1, 64, 8, 2, 64, "bf16")
+    with pytest.raises(TypeError):
+        m.hsa_prompt_fwd(x["q"], x["k"], x["v"], cu_seqlens=[0, 64])
+    with pytest.raises(TypeError):
+        m.hsa_prompt_fwd(x["q"], x["k"], None)
+    with pytest.raises(TypeError):
+        m.hsa_prompt_bwd(x["q"], x["k"], x["v"], x["q"], x["dO"], None)
+    d = decode_inputs(2, 64, 8, 8, 2, 64, "bf16", [8, 8])
+    with pytest.raises(ValueError):
+        m.hsa_prefix_decode(d["q"], d["kp"], None, d["kc"], d["vc"], d["lens"])
+    with pytest.raises(TypeError):
+        m.hsa_prefix_decode(d["q"], d["kp"], d["vp"], d["kc"], d["vc"], None)
