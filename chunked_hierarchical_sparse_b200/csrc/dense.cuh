@@ -17,6 +17,16 @@ namespace dense {
 constexpr int kSimtRows = 64;    // rows and keys of a CUDA-core tile
 constexpr int kNoMask = 0x3fffffff;  // causal offset of an item whose keys are all visible
 
+// two FMAs in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
 // Geometry and tensors of one call (passed to the kernels by value).
 struct Args {
     int decode;                  // 0: prompt pass, 1: decode over a shared prefix

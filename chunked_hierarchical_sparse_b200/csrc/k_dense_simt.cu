@@ -41,12 +41,14 @@ template <int D, typename F> __device__ __forceinline__ void load_tile(float *ds
     }
 }
 
-// acc[i][j] = A[ty + 16 i] . B[tx + 16 j] over d
+// acc[i][j] = A[ty + 16 i] . B[tx + 16 j] over d: even and odd columns of d are summed apart, two
+// FMAs an instruction
 template <int D> __device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float *A, const float *B, int ty, int tx) {
+    float2 s[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) s[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
         float4 x[4], y[4];
@@ -59,12 +61,14 @@ template <int D> __device__ __forceinline__ void dot_tile(float (&acc)[4][4], co
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
-                acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
-                acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
-                acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+                s[i][j] = fma2(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), s[i][j]);
+                s[i][j] = fma2(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), s[i][j]);
             }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = s[i][j].x + s[i][j].y;
 }
 
 // acc[i][64 h + 4 tx + e] += sum_n P[ty + 16 i][n] B[n][64 h + 4 tx + e]
@@ -85,10 +89,10 @@ __device__ __forceinline__ void accum_tile(float (&acc)[4][D / 16], const float 
                 const float4 b = *reinterpret_cast<const float4 *>(B + (n + e) * (D + 4) + h * 64 + tx * 4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    acc[i][h * 4 + 0] = fmaf(p[i][e], b.x, acc[i][h * 4 + 0]);
-                    acc[i][h * 4 + 1] = fmaf(p[i][e], b.y, acc[i][h * 4 + 1]);
-                    acc[i][h * 4 + 2] = fmaf(p[i][e], b.z, acc[i][h * 4 + 2]);
-                    acc[i][h * 4 + 3] = fmaf(p[i][e], b.w, acc[i][h * 4 + 3]);
+                    const float2 pp = make_float2(p[i][e], p[i][e]);
+                    float2 *y = reinterpret_cast<float2 *>(&acc[i][h * 4]);
+                    y[0] = fma2(pp, make_float2(b.x, b.y), y[0]);
+                    y[1] = fma2(pp, make_float2(b.z, b.w), y[1]);
                 }
             }
     }
@@ -134,7 +138,7 @@ __device__ __forceinline__ void add_tiles(const cg::cluster_group &cl, float *ti
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThr) fwd_simt_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) fwd_simt_kernel(const __grid_constant__ Args a) {
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + kT * (D + 4), *V = K + kT * (D + 4), *P = V + kT * (D + 4);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -381,11 +385,19 @@ template <int D> constexpr size_t fwd_smem() { return sizeof(float) * (3 * kT * 
 template <int D> constexpr size_t dq_smem() { return sizeof(float) * (4 * kT * (D + 4) + kT * kPS); }
 template <int D> constexpr size_t dkv_smem() { return sizeof(float) * (4 * kT * (D + 4) + 2 * kT * kPS); }
 
-// Blocks per item: as many as fill the GPU about once (`fit` blocks per SM), each with a
-// tile of the walk at least
+// Blocks per item: as many as fill the GPU about once (`fit` blocks per SM), each with a tile of
+// the walk at least.  Items' walks differ (the first keys are seen by every row), so long ones are
+// shared beyond that, by up to 4 blocks that keep 8 tiles each: the first item then ends with the
+// rest.  (Backward, one prompt of 2K tokens, 16 heads in 2 groups, d = 128, key tiles shared by 2 / 4 / 8
+// blocks: 3.46 / 2.14 / 2.31 ms -- clusters of 8 leave SMs idle --, 4 heads, d = 64: 458 / 306 / 361 us;
+// 1K tokens, forward, blocks with 4 / 2 tiles: 37 / 41 us.)
 int cluster_size(int64_t items, int walk, int fit) {
     int c = 1;
-    while (c < 8 && items * c * 2 <= fit * kPlanSms && c * 2 <= walk) c *= 2;
+    while (c < 8 && c * 2 <= walk) {
+        const int64_t blocks = items * c * 2, fill = (int64_t)fit * kPlanSms;
+        if (blocks > fill && (c >= 4 || walk < 16 * c || blocks > 2 * fill)) break;
+        c *= 2;
+    }
     return c;
 }
 
