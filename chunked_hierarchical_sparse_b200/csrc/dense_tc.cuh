@@ -60,7 +60,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64
             if (__any_sync(0xffffffffu, *abort != 0)) return false;
             if (__any_sync(0xffffffffu, at_once || globaltimer() - t0 > limit_ns)) {
                 *abort = 1;
-                report(ds, HSA_ERR_TIMEOUT, kKDense, role, 0);
+                report(ds, HSA_ERR_TIMEOUT, kKDense, role, (int)((int64_t)(globaltimer() - t0) / 1000));
                 return false;
             }
             ok = mbar_try(bar, parity);
@@ -82,7 +82,7 @@ __device__ __forceinline__ bool thread_wait(uint64_t *bar, uint32_t parity, uint
         if (*abort) return false;
         if (at_once || globaltimer() - t0 > limit_ns) {
             *abort = 1;
-            report(ds, HSA_ERR_TIMEOUT, kKDense, role, 0);
+            report(ds, HSA_ERR_TIMEOUT, kKDense, role, (int)((int64_t)(globaltimer() - t0) / 1000));
             return false;
         }
         if (mbar_try(bar, parity)) return true;

@@ -135,8 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
     uint64_t *item_full = bar, *item_empty = bar + 2, *fix_full = bar + 4, *fix_empty = bar + 5;
     uint64_t *stat_full = bar + 6, *stat_empty = bar + 8;
-    uint64_t *s_full = bar + 20, *dp_full = bar + 11, *p_full = bar + 12, *ds_full = bar + 13, *acc_full = bar + 14;
-    uint64_t *done = bar + 15, *clean = bar + 16, *clear_req = bar + 17, *p_half = bar + 18, *ring_full = bar + kBarriers, *ring_empty = ring_full + L::ST;
+    uint64_t *s_full = bar + 20, *dp_full = bar + 11, *p_full = bar + 18, *ds_full = bar + 13, *acc_full = bar + 14;
+    uint64_t *done = bar + 15, *clean = bar + 16, *clear_req = bar + 17, *p_half = bar + 10, *ring_full = bar + kBarriers, *ring_empty = ring_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
     volatile int *clear_job = abort_flag + 1;  // stage, first row
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             mbar_init(&stat_full[i], 1); mbar_init(&stat_empty[i], 8);
         }
         mbar_init(fix_full, 1); mbar_init(fix_empty, 1);
-        mbar_init(s_full, 1); mbar_init(s_full + 1, 1); mbar_init(dp_full, 1); mbar_init(p_half, 8); mbar_init(p_full, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
+        mbar_init(s_full, 1); mbar_init(s_full + 1, 1); mbar_init(dp_full, 1); mbar_init(p_half, 8); mbar_init(p_full, 8); mbar_init(p_full + 1, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
         mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
         *abort_flag = 0;
@@ -175,6 +175,11 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     dependency_wait();
     dependents_may_start();
     const uint32_t t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + D;
+    // A waiter sees a barrier's phases by their parity: the next but one must not complete before it has
+    // looked.  With S computed ahead the warpgroups may be a P further than the MMA thread has seen: two
+    // barriers, by step.  (The others' next phase needs a product issued behind the wait.)
+    auto p_done = [&](int step) { return &p_full[kTwoS ? step & 1 : 0]; };
+    auto p_phase = [&](int step) { return (uint32_t)(kTwoS ? step >> 1 : step); };
     auto t_s = [&](int step) { return tmem + (kTwoS && (step & 1) ? 384u : 0u); };
     auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
     if (warp == kWarpLoad) {
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                         mma_sum<D, 64, 0, 2>(t_dv, t_s(np), tile(d), j > j0);
                         mma_sum<D, 64, 4, 6>(t_dv, t_s(np), tile(d), 1);
                     }
-                    if (!(ok = wait1(p_full, np))) break;
+                    if (!(ok = wait1(p_done(np), p_phase(np)))) break;
                     tc_fence_after();
                     if constexpr (kTwoS) {
                         mma_sum<D, 64>(t_dv, t_s(np), tile(d), j > j0);
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    mbar_arrive_lane0(h ? p_full : p_half, lane);
+                    mbar_arrive_lane0(h ? p_done(nt) : p_half, lane);
                 }
                 if (!(ok = wait(dp_full, nt, 14))) break;
                 tc_fence_after();
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     BwdItem *items = reinterpret_cast<BwdItem *>(sm + L::OFF_ITEM);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
     uint64_t *item_full = bar, *item_empty = bar + 2, *fix_full = bar + 4, *fix_empty = bar + 5;
-    uint64_t *s_full = bar + 6, *dp_full = bar + 8, *dp_read = bar + 9, *ds_full = bar + 10, *acc_full = bar + 11;
+    uint64_t *s_full = bar + 6, *dp_full = bar + 8, *dp_read = bar + 9, *ds_full = bar + 17, *acc_full = bar + 11;
     uint64_t *done = bar + 12, *clean = bar + 13, *clear_req = bar + 14, *join = bar + 15, *out_read = bar + 16, *ring_full = bar + kBarriers, *ring_empty = ring_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 9); mbar_init(&s_full[i], 1); }
         mbar_init(fix_full, 1); mbar_init(fix_empty, 1);
-        mbar_init(dp_full, 1); mbar_init(dp_read, 8); mbar_init(ds_full, 8); mbar_init(acc_full, 1);
+        mbar_init(dp_full, 1); mbar_init(dp_read, 8); mbar_init(ds_full, 8); mbar_init(ds_full + 1, 8); mbar_init(acc_full, 1);
         mbar_init(join, 8); mbar_init(out_read, 8);
         mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
@@ -489,6 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     dependency_wait();
     dependents_may_start();
     const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;  // S: two buffers
+    // (S and dP of the next step are issued before the wait for this step's dS, so the warpgroups may
+    // finish both before the MMA thread looks: two ds_full, in turns)
     auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
     auto tiles = [](int keys) { return (keys + kTile - 1) / kTile; };
     auto sweep = [](int nt) { return nt <= kSweep ? nt : 0; };
@@ -615,7 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                         break;
                     }
                     if (j >= sw) {
-                        if (!(ok = wait1(ds_full, nd++))) break;
+                        if (!(ok = wait1(&ds_full[nd & 1], nd >> 1))) break;
+                        ++nd;
                         tc_fence_after();
                         mma_sum<D, 64>(t_dq, t_s + ((nt + j) & 1) * 128, tile(k), j > sw);
                         mma_commit(&ring_empty[k.st]);
@@ -641,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
         const uint32_t xd = t_dp + lanes + w * 64;
         const float c = a.scale_log2;
         const int rt = r / a.G, rh = r % a.G;
-        int nt = 0, na = 0, n_join = 0, pos = 0;
+        int nt = 0, na = 0, n_join = 0, pos = 0, nd = 0;
         bool ok = true;
         for (int n = 0; ok; ++n) {
             const int ib = n % kItems;
@@ -748,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                 store64(xs, x);
                 tc_fence_before();
                 __syncwarp();
-                mbar_arrive_lane0(ds_full, lane);
+                mbar_arrive_lane0(&ds_full[nd++ & 1], lane);
             }
             if (!ok || !(ok = wait(acc_full, na, 24))) break;
             ++na;

@@ -555,3 +555,26 @@ def test_missing_tensors_are_refused():
         m.hsa_prefix_decode(d["q"], d["kp"], None, d["kc"], d["vc"], d["lens"])
     with pytest.raises(TypeError):
         m.hsa_prefix_decode(d["q"], d["kp"], d["vp"], d["kc"], d["vc"], None)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_calls_in_a_row(d):
+    """No wait of a kernel may depend on how fast its roles run beside one another: thousands
+    of calls, queued without a pause, report nothing and give the same bits."""
+    m = hsa()
+    x = inputs(1, 889, 6, 3, d, "bf16", seed=d)
+    b = buffers(x)
+    ws = {op: torch.empty(m.hsa_prompt_workspace_size(1, 889, 6, 3, d, torch.bfloat16, op), dtype=torch.uint8, device=DEV)
+          for op in (m.OP_FWD, m.OP_BWD)}
+    worst, first = torch.zeros(1, dtype=torch.int32, device=DEV), None
+    for i in range(4000):
+        m.hsa_prompt_fwd(x["q"], x["k"], x["v"], o=b["o"], lse=b["lse"], ws=ws[m.OP_FWD])
+        m.hsa_prompt_bwd(x["q"], x["k"], x["v"], b["o"], x["dO"], b["lse"], dq=b["dq"], dk=b["dk"], dv=b["dv"],
+                         ws=ws[m.OP_BWD])
+        for w in ws.values():
+            torch.maximum(worst, w[:4].view(torch.int32), out=worst)
+        if i == 0:
+            first = {n: t.clone() for n, t in b.items()}
+    assert int(worst) == 0
+    for n, t in b.items():
+        assert torch.equal(t, first[n]), n
