@@ -271,10 +271,10 @@ hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, cons
     if (!empty && !all_ok({q, k, v, o, dO, lse, dq, dk, dv})) return HSA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const PromptWs w = carve_prompt(*shape, ws, true);
-    const bool planned = w.kplan != nullptr;  // the plan kernel clears the header itself
-    cudaError_t e = empty || !planned ? cudaMemsetAsync(ws, 0, kWsHeader, st) : cudaSuccess;
+    const bool planned = w.kplan != nullptr, tc = tensor_cores(*shape);
+    // (the plan kernel and the fp32 kernels clear the header themselves)
+    cudaError_t e = empty || (tc && !planned) ? cudaMemsetAsync(ws, 0, kWsHeader, st) : cudaSuccess;
     if (empty || e != cudaSuccess) return cuda_status(e);
-    const bool tc = tensor_cores(*shape);
     BwdArgs b{};
     b.a = prompt_args(*shape, q, k, v, ws, w, bwd_tok(*shape));
     b.kplan = w.kplan;

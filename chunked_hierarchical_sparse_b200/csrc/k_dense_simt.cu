@@ -125,16 +125,21 @@ __device__ __forceinline__ void add4(float4 &v, float4 x, float f) {
 }
 // Sums a tile that every block of the cluster holds at the same place, in rank order; the
 // calling block's 64 / C rows of it go, scaled, to dst(row) + column.
-template <int D, typename F>
+template <int D, int THREADS, typename F>
 __device__ __forceinline__ void add_tiles(const cg::cluster_group &cl, float *tile, int rows, float scale, F &&dst) {
     const int C = cl.num_blocks(), rank = cl.block_rank();
-    for (int i = threadIdx.x; i < kT / C * (D / 4); i += kThr) {
+    for (int i = threadIdx.x; i < kT / C * (D / 4); i += THREADS) {
         const int r = rank * (kT / C) + i / (D / 4), c = i % (D / 4) * 4;
         if (r >= rows) break;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int q = 0; q < C; ++q) add4(v, *reinterpret_cast<const float4 *>(cl.map_shared_rank(tile, q) + r * (D + 4) + c), 1.f);
         store4(dst(r) + c, make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale));
     }
+}
+
+// (the kernels here keep no counters in the header and report nothing, so any block may clear it)
+__device__ __forceinline__ void clear_header(DevStatus *ds) {
+    if (threadIdx.x < kHeaderWords) reinterpret_cast<int32_t *>(ds)[threadIdx.x] = 0;
 }
 
 template <int D>
@@ -147,6 +152,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) fwd_simt_kernel(const _
     dependents_may_start();
     const cg::cluster_group cl = cg::this_cluster();
     const int rank = cl.block_rank(), C = cl.num_blocks(), item = blockIdx.x / C;
+    if (!a.plan && blockIdx.x == 0) clear_header(a.ds);
     if (item >= item_count(a) || !get_item(a, item, it)) return;  // (the whole cluster)
     const int rows = it.ntok * a.G;
     const float *q = static_cast<const float *>(a.q);
@@ -245,13 +251,14 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) fwd_simt_kernel(const _
     cl.sync();  // no block leaves while another reads its memory
 }
 
-// delta[row] = dO . o, one warp per (token, head) row
+// delta[row] = dO . o, one warp per (token, head) row; `header`: to be cleared (null: by a kernel before)
 template <int D>
-__global__ void __launch_bounds__(256) delta_kernel(const float *o, const float *dO, float *delta, int64_t rows) {
+__global__ void __launch_bounds__(256) delta_kernel(const float *o, const float *dO, float *delta, int64_t rows, DevStatus *header) {
     const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     dependency_wait();
     dependents_may_start();
+    if (header && blockIdx.x == 0) clear_header(header);
     if (r >= rows) return;
     float s = 0.f;
 #pragma unroll
@@ -265,13 +272,88 @@ __global__ void __launch_bounds__(256) delta_kernel(const float *o, const float 
     if (lane == 0) delta[r] = s;
 }
 
+// The backward's two kernels run two groups of 256 threads: one computes S and p, the other dP, on
+// different products at the same time.  A step of a small problem is latency, and 8 warps hide little
+// of it: one prompt of 1K tokens, 4 heads in a group, 209 us with one group doing both, 150 with two.
+// (d = 64, 8K tokens, two such blocks per SM: 15.4 ms, now 16.4; d = 128, 16 x 1K tokens: 9.1, now 7.8.)  Masked places are zeros in both.  The next tiles wait in registers meanwhile.
+constexpr int kThr2 = 2 * kThr;
+
+// A 64 x D tile on its way from global memory to a padded one: each thread's part
+template <int D> struct Fetch {
+    static constexpr int V = D / 4, N = kT * V / kThr2;
+    float4 x[N];
+    template <typename F> __device__ __forceinline__ void load(F &&src) {  // row r comes from src(r) (null: zeros)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = threadIdx.x + i * kThr2;
+            const float *p = src(at / V);
+            x[i] = p ? *reinterpret_cast<const float4 *>(p + at % V * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    __device__ __forceinline__ void store(float *dst) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = threadIdx.x + i * kThr2;
+            store4(dst + at / V * (D + 4) + at % V * 4, x[i]);
+        }
+    }
+};
+
+// acc[i][] += sum_n P[ty + 16 i][n] B[n][columns of tx].  W columns of B's D: 4 per thread of every 64
+// (W = 32: 2).
+template <int D, int W>
+__device__ __forceinline__ void accum2(float2 (&acc)[4][W / 32], const float *P, const float *B, int ty, int tx) {
+#pragma unroll 1
+    for (int n = 0; n < kT; n += 4) {
+        float p[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 v = *reinterpret_cast<const float4 *>(P + (ty + 16 * i) * kPS + n);
+            p[i][0] = v.x; p[i][1] = v.y; p[i][2] = v.z; p[i][3] = v.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float2 b[W / 32];
+            const float *row = B + (n + e) * (D + 4);
+            if constexpr (W == 32) {
+                b[0] = *reinterpret_cast<const float2 *>(row + tx * 2);
+            } else {
+#pragma unroll
+                for (int h = 0; h < W / 64; ++h) {
+                    const float4 x = *reinterpret_cast<const float4 *>(row + h * 64 + tx * 4);
+                    b[2 * h] = make_float2(x.x, x.y);
+                    b[2 * h + 1] = make_float2(x.z, x.w);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < W / 32; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][h] = fma2(make_float2(p[i][e], p[i][e]), b[h], acc[i][h]);
+        }
+    }
+}
+// the accumulator's W columns into a padded tile
+template <int D, int W> __device__ __forceinline__ void put2(float *dst, const float2 (&acc)[4][W / 32], int ty, int tx) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float *row = dst + (ty + 16 * i) * (D + 4);
+        if constexpr (W == 32) {
+            *reinterpret_cast<float2 *>(row + tx * 2) = acc[i][0];
+        } else {
+#pragma unroll
+            for (int h = 0; h < W / 64; ++h)
+                store4(row + h * 64 + tx * 4, make_float4(acc[i][2 * h].x, acc[i][2 * h].y, acc[i][2 * h + 1].x, acc[i][2 * h + 1].y));
+        }
+    }
+}
+
 // dq of a row tile: walks the keys, dq += (p (dO.v - delta)) k
 template <int D>
-__global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dq_simt_kernel(const __grid_constant__ BwdArgs b) {
+__global__ void __launch_bounds__(kThr2, 1) bwd_dq_simt_kernel(const __grid_constant__ BwdArgs b) {
     extern __shared__ float sm[];
     const Args &a = b.a;
     float *Q = sm, *G = Q + kT * (D + 4), *K = G + kT * (D + 4), *V = K + kT * (D + 4), *S = V + kT * (D + 4);
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int grp = threadIdx.x / kThr, ty = threadIdx.x % kThr >> 4, tx = threadIdx.x & 15;
     Item it;
     dependency_wait();
     dependents_may_start();
@@ -282,54 +364,76 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dq_simt_kernel(cons
     const int64_t pl = it.plane * a.plane[0] + (int64_t)it.key0 * D;
     const float *kp = static_cast<const float *>(a.k[0]) + pl, *vp = static_cast<const float *>(a.v[0]) + pl;
     auto row_index = [&](int r) { return ((int64_t)it.tok0 + r / a.G) * a.hq + it.g * a.G + r % a.G; };
-    load_tile<D>(Q, [&](int r) -> const float * { return r < rows ? static_cast<const float *>(a.q) + row_index(r) * D : nullptr; });
-    load_tile<D>(G, [&](int r) -> const float * { return r < rows ? static_cast<const float *>(b.dO) + row_index(r) * D : nullptr; });
-    float l2[4], de[4], dq[4][D / 16];
+    Fetch<D> fk, fv;
+    auto fetch = [&](int n0) {  // (behind the last key: zeros)
+        auto key = [&](const float *p, int r) -> const float * { return n0 + r < it.nkeys ? p + (int64_t)(n0 + r) * D : nullptr; };
+        fk.load([&](int r) { return key(kp, r); });
+        fv.load([&](int r) { return key(vp, r); });
+    };
+    {
+        auto row = [&](const void *p, int r) -> const float * { return r < rows ? static_cast<const float *>(p) + row_index(r) * D : nullptr; };
+        fk.load([&](int r) { return row(a.q, r); });
+        fv.load([&](int r) { return row(b.dO, r); });
+        fk.store(Q);
+        fv.store(G);
+    }
+    fetch(rank * kT);
+    float st[4];  // group 0: lse, 1: delta
+    float2 dq[4][D / 64];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = ty + 16 * i;
-        l2[i] = r < rows ? b.lse[row_index(r)] * 1.4426950408889634f : INFINITY;
-        de[i] = r < rows ? b.delta[row_index(r)] : 0.f;
+        if (grp == 0) st[i] = r < rows ? b.lse[row_index(r)] * 1.4426950408889634f : INFINITY;
+        else st[i] = r < rows ? b.delta[row_index(r)] : 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) dq[i][c] = 0.f;
+        for (int c = 0; c < D / 64; ++c) dq[i][c] = make_float2(0.f, 0.f);
     }
     for (int n0 = rank * kT; n0 < it.nkeys; n0 += C * kT) {
         __syncthreads();
-        auto key = [&](const float *p, int r) -> const float * { return n0 + r < it.nkeys ? p + (int64_t)(n0 + r) * D : nullptr; };
-        load_tile<D>(K, [&](int r) { return key(kp, r); });
-        load_tile<D>(V, [&](int r) { return key(vp, r); });
+        fk.store(K);
+        fv.store(V);
         __syncthreads();
-        float s[4][4], dp[4][4];
-        dot_tile<D>(s, Q, K, ty, tx);
-        dot_tile<D>(dp, G, V, ty, tx);
+        if (n0 + C * kT < it.nkeys) fetch(n0 + C * kT);
+        float s[4][4];
+        dot_tile<D>(s, grp ? G : Q, grp ? V : K, ty, tx);
+        // each group gives the other half of its values and multiplies the other half
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int last = it.off + (ty + 16 * i) / a.G;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int n = n0 + tx + 16 * j;
-                const float p = exp2f(s[i][j] * a.scale_log2 - l2[i]);
-                S[(ty + 16 * i) * kPS + tx + 16 * j] = n < it.nkeys && n <= last ? p * (dp[i][j] - de[i]) : 0.f;
+                const float x = grp ? s[i][j] - st[i] : exp2f(s[i][j] * a.scale_log2 - st[i]);
+                s[i][j] = n < it.nkeys && n <= last ? x : 0.f;
+                if (j / 2 != grp) S[(ty + 16 * i) * kPS + tx + 16 * j] = s[i][j];
             }
         }
         __syncthreads();
-        accum_tile<D>(dq, S, K, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float *y = S + (ty + 16 * i) * kPS + tx + 16 * j + 32 * grp;
+                *y *= grp ? s[i][j + 2] : s[i][j];
+            }
+        __syncthreads();
+        accum2<D, D / 2>(dq, S, K + grp * (D / 2), ty, tx);  // half of the columns each
     }
     __syncthreads();
-    put_tile<D>(K, dq, ty, tx);
+    put2<D, D / 2>(K + grp * (D / 2), dq, ty, tx);
     cl.sync();
-    add_tiles<D>(cl, K, rows, a.scale, [&](int r) { return static_cast<float *>(b.dq) + row_index(r) * D; });
+    add_tiles<D, kThr2>(cl, K, rows, a.scale, [&](int r) { return static_cast<float *>(b.dq) + row_index(r) * D; });
     cl.sync();
 }
 
 // dk, dv of a tile of keys: walks the row tiles that see it, all heads of the group
 template <int D>
-__global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dkv_simt_kernel(const __grid_constant__ BwdArgs b) {
+__global__ void __launch_bounds__(kThr2, 1) bwd_dkv_simt_kernel(const __grid_constant__ BwdArgs b) {
     extern __shared__ float sm[];
     const Args &a = b.a;
     float *K = sm, *V = K + kT * (D + 4), *Q = V + kT * (D + 4), *G = Q + kT * (D + 4), *P = G + kT * (D + 4),
           *S = P + kT * kPS;
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int grp = threadIdx.x / kThr, ty = threadIdx.x % kThr >> 4, tx = threadIdx.x & 15;
     KeyItem it;
     dependency_wait();
     dependents_may_start();
@@ -337,53 +441,81 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) bwd_dkv_simt_kernel(con
     const int rank = cl.block_rank(), C = cl.num_blocks(), item = blockIdx.x / C;
     if (item >= key_item_count(b) || !get_key_item(b, item, kT, it)) return;
     const int64_t pl = it.plane * a.plane[0] + (int64_t)(it.start + it.n0) * D;
-    load_tile<D>(K, [&](int r) -> const float * { return r < it.nkeys ? static_cast<const float *>(a.k[0]) + pl + r * D : nullptr; });
-    load_tile<D>(V, [&](int r) -> const float * { return r < it.nkeys ? static_cast<const float *>(a.v[0]) + pl + r * D : nullptr; });
-    float dk[4][D / 16], dv[4][D / 16];
+    Fetch<D> fq, fg;
+    auto row_index = [&](int t0, int r) { return (it.row0 + t0 + r / a.G) * a.hq + it.g * a.G + r % a.G; };
+    auto rows_at = [&](int t0) { return min(a.tok, it.len - t0) * a.G; };
+    auto fetch = [&](int t0) {
+        const int rows = rows_at(t0);
+        auto row = [&](const void *p, int r) -> const float * { return r < rows ? static_cast<const float *>(p) + row_index(t0, r) * D : nullptr; };
+        fq.load([&](int r) { return row(a.q, r); });
+        fg.load([&](int r) { return row(b.dO, r); });
+    };
+    {
+        auto key = [&](const void *p, int r) -> const float * { return r < it.nkeys ? static_cast<const float *>(p) + pl + r * D : nullptr; };
+        fq.load([&](int r) { return key(a.k[0], r); });
+        fg.load([&](int r) { return key(a.v[0], r); });
+        fq.store(K);
+        fg.store(V);
+    }
+    const int t_first = it.n0 + rank * a.tok;
+    if (t_first < it.len) fetch(t_first);
+    float2 acc[4][D / 32];  // group 0: dv, 1: dk
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
-    for (int t0 = it.n0 + rank * a.tok; t0 < it.len; t0 += C * a.tok) {
-        const int rows = min(a.tok, it.len - t0) * a.G;
-        auto row_index = [&](int r) { return (it.row0 + t0 + r / a.G) * a.hq + it.g * a.G + r % a.G; };
+        for (int c = 0; c < D / 32; ++c) acc[i][c] = make_float2(0.f, 0.f);
+    for (int t0 = t_first; t0 < it.len; t0 += C * a.tok) {
+        const int rows = rows_at(t0);
         __syncthreads();
-        load_tile<D>(Q, [&](int r) -> const float * { return r < rows ? static_cast<const float *>(a.q) + row_index(r) * D : nullptr; });
-        load_tile<D>(G, [&](int r) -> const float * { return r < rows ? static_cast<const float *>(b.dO) + row_index(r) * D : nullptr; });
+        fq.store(Q);
+        fg.store(G);
         __syncthreads();
-        float s[4][4], dp[4][4];  // keys down, rows across: the sums below read P and S along their rows
-        dot_tile<D>(s, K, Q, ty, tx);
-        dot_tile<D>(dp, V, G, ty, tx);
+        float st[4];  // group 0: lse, 1: delta, of the rows (columns of the tile)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int r = tx + 16 * j;
-            const float l2 = r < rows ? b.lse[row_index(r)] * 1.4426950408889634f : INFINITY;
-            const float de = r < rows ? b.delta[row_index(r)] : 0.f;
+            if (grp == 0) st[j] = r < rows ? b.lse[row_index(t0, r)] * 1.4426950408889634f : INFINITY;
+            else st[j] = r < rows ? b.delta[row_index(t0, r)] : 0.f;
+        }
+        if (t0 + C * a.tok < it.len) fetch(t0 + C * a.tok);
+        float s[4][4];  // keys down, rows across: the sums below read P and S along their rows
+        dot_tile<D>(s, grp ? V : K, grp ? G : Q, ty, tx);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = tx + 16 * j, tok = t0 + r / a.G - it.n0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int n = ty + 16 * i;
-                const bool seen = r < rows && n < it.nkeys && it.n0 + n <= t0 + r / a.G;
-                const float p = seen ? exp2f(s[i][j] * a.scale_log2 - l2) : 0.f;
-                P[n * kPS + r] = p;
-                S[n * kPS + r] = seen ? p * (dp[i][j] - de) : 0.f;
+                const float x = grp ? s[i][j] - st[j] : exp2f(s[i][j] * a.scale_log2 - st[j]);
+                s[i][j] = r < rows && n < it.nkeys && n <= tok ? x : 0.f;
+                if (grp == 0) P[n * kPS + r] = s[i][j];
             }
         }
         __syncthreads();
-        accum_tile<D>(dv, P, G, ty, tx);
-        accum_tile<D>(dk, S, Q, ty, tx);
+        if (grp == 0) {
+            accum2<D, D>(acc, P, G, ty, tx);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = (ty + 16 * i) * kPS + tx + 16 * j;
+                    S[at] = P[at] * s[i][j];
+                }
+            asm volatile("bar.sync 1, 256;" ::: "memory");  // (the group)
+            accum2<D, D>(acc, S, Q, ty, tx);
+        }
     }
     __syncthreads();
-    put_tile<D>(K, dv, ty, tx);
-    put_tile<D>(V, dk, ty, tx);
+    put2<D, D>(grp ? V : K, acc, ty, tx);
     cl.sync();
-    add_tiles<D>(cl, K, it.nkeys, 1.f, [&](int r) { return static_cast<float *>(b.dv) + pl + (int64_t)r * D; });
-    add_tiles<D>(cl, V, it.nkeys, a.scale, [&](int r) { return static_cast<float *>(b.dk) + pl + (int64_t)r * D; });
+    add_tiles<D, kThr2>(cl, K, it.nkeys, 1.f, [&](int r) { return static_cast<float *>(b.dv) + pl + (int64_t)r * D; });
+    add_tiles<D, kThr2>(cl, V, it.nkeys, a.scale, [&](int r) { return static_cast<float *>(b.dk) + pl + (int64_t)r * D; });
     cl.sync();
 }
 
 template <int D> constexpr size_t fwd_smem() { return sizeof(float) * (3 * kT * (D + 4) + kT * kPS); }
-template <int D> constexpr size_t dq_smem() { return sizeof(float) * (4 * kT * (D + 4) + kT * kPS); }
-template <int D> constexpr size_t dkv_smem() { return sizeof(float) * (4 * kT * (D + 4) + 2 * kT * kPS); }
+template <int D> constexpr size_t bwd_smem() { return sizeof(float) * (4 * kT * (D + 4) + 2 * kT * kPS); }
 
 // Blocks per item: as many as fill the GPU about once (`fit` blocks per SM), each with a tile of
 // the walk at least.  Items' walks differ (the first keys are seen by every row), so long ones are
@@ -404,25 +536,24 @@ int cluster_size(int64_t items, int walk, int fit) {
 template <int D> cudaError_t fwd(const Args &a, int64_t items, cudaStream_t st) {
     cudaError_t e = set_smem_once((const void *)fwd_simt_kernel<D>, fwd_smem<D>());
     if (e != cudaSuccess) return e;
-    if (!a.plan && (e = cudaMemsetAsync(a.ds, 0, kWsHeader, st)) != cudaSuccess) return e;
     const int c = a.decode ? 1 : cluster_size(items, (int)ceil_div(a.L, kT), D == 64 ? 2 : 1);
     return launch_next(a.plan != nullptr, fwd_simt_kernel<D>, (int)items * c, kThr, fwd_smem<D>(), st, c, a);
 }
 
 template <int D> cudaError_t delta(const BwdArgs &b, cudaStream_t st) {
     const int64_t rows = (int64_t)b.a.B * b.a.L * b.a.hq;
-    return launch_next(b.a.plan || b.kplan, delta_kernel<D>, (int)ceil_div(rows, 8), 256, 0, st, 1,
-                       static_cast<const float *>(b.o), static_cast<const float *>(b.dO), b.delta, rows);
+    return launch_next(b.a.plan != nullptr, delta_kernel<D>, (int)ceil_div(rows, 8), 256, 0, st, 1,
+                       static_cast<const float *>(b.o), static_cast<const float *>(b.dO), b.delta, rows, b.a.plan ? nullptr : b.a.ds);
 }
 
 template <int D> cudaError_t bwd(const BwdArgs &b, int64_t row_items, int64_t key_items, cudaStream_t st) {
-    cudaError_t e = set_smem_once((const void *)bwd_dq_simt_kernel<D>, dq_smem<D>());
-    if (e == cudaSuccess) e = set_smem_once((const void *)bwd_dkv_simt_kernel<D>, dkv_smem<D>());
+    cudaError_t e = set_smem_once((const void *)bwd_dq_simt_kernel<D>, bwd_smem<D>());
+    if (e == cudaSuccess) e = set_smem_once((const void *)bwd_dkv_simt_kernel<D>, bwd_smem<D>());
     if (e != cudaSuccess) return e;
-    const int ck = cluster_size(key_items, (int)ceil_div(b.a.L, b.a.tok), D == 64 ? 2 : 1), cr = cluster_size(row_items, (int)ceil_div(b.a.L, kT), D == 64 ? 2 : 1);
-    e = launch_next(true, bwd_dkv_simt_kernel<D>, (int)key_items * ck, kThr, dkv_smem<D>(), st, ck, b);
+    const int ck = cluster_size(key_items, (int)ceil_div(b.a.L, b.a.tok), 1), cr = cluster_size(row_items, (int)ceil_div(b.a.L, kT), 1);
+    e = launch_next(true, bwd_dkv_simt_kernel<D>, (int)key_items * ck, kThr2, bwd_smem<D>(), st, ck, b);
     if (e != cudaSuccess) return e;
-    return launch_next(true, bwd_dq_simt_kernel<D>, (int)row_items * cr, kThr, dq_smem<D>(), st, cr, b);
+    return launch_next(true, bwd_dq_simt_kernel<D>, (int)row_items * cr, kThr2, bwd_smem<D>(), st, cr, b);
 }
 
 }  // namespace
