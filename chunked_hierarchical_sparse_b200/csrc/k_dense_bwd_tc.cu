@@ -17,13 +17,16 @@
 //   of the same tiles, so dK and dV of shared heads are summed by the products.
 // - row pass: 128 (token, head) rows per CTA, walking the keys: S, dP, then
 //   dQ += dS K.  S has two buffers, so the tensor cores run ahead of the exponentials.
-// D (written by the row pass, which goes first).  Taken from the stored output (dO . o) it carries o's rounding to bf16, 2^-9 of |dO||o|,
-// into every dS of the row; that is small where a row averages many values and the largest
-// single error where it averages few.  The row pass therefore first sweeps the keys of rows
-// that have at most kSweep tiles of them for D = sum p dP (two products more per tile, on a
-// fraction of any long prompt) and leaves it to the key pass.  Relative error of dq against 64
-// bits: prompts of 12 tokens 0.0031 -> 0.0025, 16K tokens 0.0026 -> 0.0024 (rounding dq alone:
-// 0.0017; eight tiles instead of two gain 0.00002), for about 2 us a call.
+// D is written by the row pass, which goes first.  Taken from the stored output (dO . o) it
+// carries o's rounding to bf16, 2^-9 of |dO||o|, into every dS of the row; that is small where a
+// row averages many values and the largest single error where it averages few.  The row pass
+// therefore first sweeps the keys of rows that have at most kSweep tiles of them for D = sum p dP
+// (two products more per tile, on a fraction of any long prompt).  The same rows' dS, an operand in
+// bf16, keeps in the columns beside it what its rounding takes off, for one product more in either
+// pass.  Relative errors of dq and dk against 64 bits (rounding the exact values alone: 0.0017):
+// neither 0.0031 (12 tokens), 0.0026 (16K tokens); the sweep 0.0025, 0.0024; both 0.0017, 0.0022.
+// The sweep takes about 2 us of a call, the remainders 2 more (2K tokens: 86 -> 88 us); eight tiles
+// instead of two gain 0.00002.
 // Two compute warpgroups take half of a tile's columns each (64 values of S and of dP
 // per thread); the MMAs are issued so that one warpgroup step always has one or two
 // products running behind it.
@@ -71,6 +74,21 @@ __device__ __forceinline__ void store64(uint32_t t, const float (&x)[64]) {  // 
 #pragma unroll
     for (int i = 0; i < 32; ++i) u[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
     tmem_st32(t, u);
+    tmem_wait_st();
+}
+// what store64 rounded off, as bf16 pairs in the 32 columns behind its own
+__device__ __forceinline__ void store64_rest(uint32_t t, const float (&x)[64]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t u[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float a = x[32 * h + 2 * i], b = x[32 * h + 2 * i + 1];
+            const uint32_t p = bf16_pair(a, b);
+            u[i] = bf16_pair(a - __uint_as_float(p << 16), b - __uint_as_float(p & 0xffff0000u));
+        }
+        tmem_st16(t + 32 + 16 * h, u);
+    }
     tmem_wait_st();
 }
 __device__ __forceinline__ float dot8(uint4 a, uint4 b) {  // eight bf16 products
@@ -180,6 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     // barriers, by step.  (The others' next phase needs a product issued behind the wait.)
     auto p_done = [&](int step) { return &p_full[kTwoS ? step & 1 : 0]; };
     auto p_phase = [&](int step) { return (uint32_t)(kTwoS ? step >> 1 : step); };
+    // row tile j's rows have at most kSweep key tiles: dS keeps what its rounding takes off (as in the row pass)
+    auto few_keys = [&](const BwdItem &t, int j) { return min((j + 1) * tt, t.ntok) <= kSweep * kTile; };
     auto t_s = [&](int step) { return tmem + (kTwoS && (step & 1) ? 384u : 0u); };
     auto wait = [&](uint64_t *x, uint32_t par, int role) { return warp_wait(x, par & 1, wait_ns, abort_flag, a.ds, role); };
     if (warp == kWarpLoad) {
@@ -304,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                     if (!(ok = wait1(ds_full, np++))) break;
                     tc_fence_after();
                     mma_sum<D, 64>(t_dk, t_dp, tile(q), j > j0);
+                    if (few_keys(t, j)) mma_sum<D, 64>(t_dk, t_dp + 32, tile(q), 1);
                     mma_commit(&ring_empty[q.st]);
                     if (more) {
                         if (!(ok = take(j + 1, d))) break;
@@ -419,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                     x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = v.x; x[4 * i + 3] = v.y;
                 }
                 store64(xd, x);
+                if (few_keys(t, j)) store64_rest(xd, x);
                 tc_fence_before();
                 __syncwarp();
                 mbar_arrive_lane0(ds_full, lane);
@@ -626,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                         ++nd;
                         tc_fence_after();
                         mma_sum<D, 64>(t_dq, t_s + ((nt + j) & 1) * 128, tile(k), j > sw);
+                        if (sw) mma_sum<D, 64>(t_dq, t_s + ((nt + j) & 1) * 128 + 32, tile(k), 1);
                         mma_commit(&ring_empty[k.st]);
                         if (j == nn - 1) mma_commit(acc_full);
                     }
@@ -754,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                     for (int i = 0; i < 64; ++i) x[i] = i <= last ? x[i] : 0.f;
                 }
                 store64(xs, x);
+                if (sw) store64_rest(xs, x);
                 tc_fence_before();
                 __syncwarp();
                 mbar_arrive_lane0(&ds_full[nd++ & 1], lane);

@@ -208,9 +208,10 @@ HSA_API hsa_status_t hsa_bwd(const hsa_shape_t *shape, const void *q, const void
  * B * h_q < 2^24 and P, cap < 2^30.  Outputs may not overlap inputs.
  *
  * Logits, softmax statistics and all sums are fp32.  In bf16 the probabilities
- * (and, in the backward, their gradients) are rounded to bf16 once, as operands of
- * the second product: the tensor cores multiply operands of one type, and the
- * values they meet are bf16 too.  Results are the same bit for bit on every call. */
+ * (and, in the backward, their gradients, but for rows of at most 256 keys, whose
+ * remainders are multiplied too) are rounded to bf16 once, as operands of the
+ * second product: the tensor cores multiply operands of one type, and the values
+ * they meet are bf16 too.  Results are the same bit for bit on every call. */
 
 typedef struct {
     int32_t B;          /* batch rows                                            */
