@@ -217,6 +217,19 @@ template <int N> struct Ring {
     }
 };
 
+// The last loads issued into a ring of `stages` tiles have landed (bounded).  Every loader
+// waits for its own before it leaves, also when all went well for it: another role may have
+// given up on them, and the CTA's shared memory is the next CTA's once all roles are done.
+__device__ __forceinline__ void land(uint64_t *full, int issued, int stages) {
+    for (int i = max(0, issued - stages); i < issued; ++i) mbar_wait(&full[i % stages], (i / stages) & 1, kDrainWaitNs);
+}
+// Likewise the products that this thread has issued: it waits for them before it leaves, so
+// that none is running when tensor memory is freed.
+__device__ __forceinline__ void finish_mma(uint64_t *done) {
+    mma_commit(done);
+    mbar_wait(done, 0, kDrainWaitNs);
+}
+
 // Rows of a ring's tile that are summed over but belong to something else are set to
 // zero by a warp of its own, at the request of the (single) MMA thread, which has seen
 // the tile arrive and waits for `clean` before the product that reads it.  job: the

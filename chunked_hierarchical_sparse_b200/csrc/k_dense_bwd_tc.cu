@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             if (lane == 0) i = atomicAdd(next, 1);
             idx = __shfl_sync(0xffffffffu, i, 0) + gridDim.x;
         }
-        if (!ok && lane == 0) {  // the loads in flight land before the CTA goes away (bounded)
-            for (int i = max(0, pos - L::ST); i < pos; ++i) mbar_wait(&ring_full[i % L::ST], (i / L::ST) & 1, kDrainWaitNs);
-            if (fixes) mbar_wait(fix_full, (fixes - 1) & 1, kDrainWaitNs);
+        if (lane == 0) {
+            land(ring_full, pos, L::ST);
+            land(fix_full, fixes, 1);
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -339,10 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                 }
             }
             request_clear(clear_req, clear_job, -1, 0);
-            if (!ok) {  // the MMAs issued so far end before tensor memory is freed (bounded)
-                mma_commit(done);
-                mbar_wait(done, 0, kDrainWaitNs);
-            }
+            finish_mma(done);
         }
         __syncwarp();
     } else if (warp == kWarpClear) {
@@ -578,9 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
             if (lane == 0) i = atomicAdd(next, 1);
             idx = __shfl_sync(0xffffffffu, i, 0) + gridDim.x;
         }
-        if (!ok && lane == 0) {
-            for (int i = max(0, pos - L::ST); i < pos; ++i) mbar_wait(&ring_full[i % L::ST], (i / L::ST) & 1, kDrainWaitNs);
-            if (fixes) mbar_wait(fix_full, (fixes - 1) & 1, kDrainWaitNs);
+        if (lane == 0) {
+            land(ring_full, pos, L::ST);
+            land(fix_full, fixes, 1);
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -657,10 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                 nt += nn;
             }
             request_clear(clear_req, clear_job, -1, 0);
-            if (!ok) {  // the MMAs issued so far end before tensor memory is freed (bounded)
-                mma_commit(done);
-                mbar_wait(done, 0, kDrainWaitNs);
-            }
+            finish_mma(done);
         }
         __syncwarp();
     } else if (warp == kWarpClear) {

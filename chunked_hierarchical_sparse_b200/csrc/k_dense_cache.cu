@@ -111,8 +111,7 @@ __global__ void __launch_bounds__(kThreads) cache_kernel(const __grid_constant__
                 }
             }
         }
-        if (!ok && lane == 0)  // the loads in flight land before the CTA goes away (bounded)
-            for (int i = max(0, j - L::ST); i < j; ++i) mbar_wait(&full[i % L::ST], (i / L::ST) & 1, kDrainWaitNs);
+        if (lane == 0) land(full, j, L::ST);
         __syncwarp();
     } else {
         // ============================================================ 16 keys of every stage

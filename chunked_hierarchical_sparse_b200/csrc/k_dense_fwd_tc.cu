@@ -222,9 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                     }
                 }
             }
-            if (!ok && lane == 0) {  // the loads in flight land before the CTA goes away (bounded)
-                for (int i = max(0, kv - L::ST); i < kv; ++i) mbar_wait(&kv_full[i % L::ST], (i / L::ST) & 1, kDrainWaitNs);
-            }
+            if (lane == 0) land(kv_full, kv, L::ST);
             __syncwarp();
         } else if (warp == kWarpQ) {
             // ======================================================== rows of Q (beside the other loads, so that
@@ -251,9 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                     ++nq[s];
                 }
             }
-            if (!ok && lane == 0)
-                for (int s = 0; s < 2; ++s)
-                    if (nq[s]) mbar_wait(&q_full[s], (nq[s] - 1) & 1, kDrainWaitNs);
+            if (lane == 0)
+                for (int s = 0; s < 2; ++s) land(&q_full[s], nq[s], 1);
             __syncwarp();
         } else if (warp == kWarpMma) {
             // ======================================================== MMA issue, a single thread
@@ -339,10 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                     }
                 }
                 request_clear(clear_req, clear_job, -1, 0);
-                if (!ok) {  // the MMAs issued so far end before tensor memory is freed (bounded)
-                    mma_commit(done);
-                    mbar_wait(done, 0, kDrainWaitNs);
-                }
+                finish_mma(done);
             }
             __syncwarp();
         } else if (warp == kWarpClear) {

@@ -1,0 +1,40 @@
+"""Dense attention on the GPU where its calls are at their limits: waits that run out early,
+bad values at the edges of tiles, sizes that take the kernels' other paths.  References and
+bounds as in test_dense_attention."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import dense_testutil as dt
+from test_dense_attention import DEV, cu_of, decode_inputs, f64, hsa, inputs, run_decode, run_prompt
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("L,G,d", [(1, 8, 128), (100, 8, 128), (130, 3, 64), (300, 16, 128), (520, 1, 64)])
+def test_waits_that_run_out_with_every_load_issued(L, G, d):
+    """Walks of so few tiles that the loaders have issued everything when the other roles give
+    up: each call waits for its copies and products, and the calls behind it are right."""
+    m = hsa()
+    x = inputs(1, L, 2 * G, 2, d, "bf16", seed=L)
+    dx = decode_inputs(3, 2 * L, 100, 2 * G, 2, d, "bf16", [100, 0, 7], seed=L)
+    good, gd = run_prompt(x), run_decode(dx)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
+    for _ in range(20):
+        codes = []
+        m.hsa_set_wait_limit_ns(1)
+        try:
+            m.hsa_prompt_fwd(x["q"], x["k"], x["v"], ws=ws)
+            codes.append(m.hsa_device_status(ws))
+            m.hsa_prompt_bwd(x["q"], x["k"], x["v"], good["o"], x["dO"], good["lse"], ws=ws)
+            codes.append(m.hsa_device_status(ws))
+            m.hsa_prefix_decode(dx["q"], dx["kp"], dx["vp"], dx["kc"], dx["vc"], dx["lens"], ws=ws)
+            codes.append(m.hsa_device_status(ws))
+        finally:
+            m.hsa_set_wait_limit_ns(0)
+        assert codes == [5, 5, 5]
+        again, gd2 = run_prompt(x), run_decode(dx)
+        assert all(torch.equal(good[n], again[n]) for n in good) and torch.equal(gd["o"], gd2["o"])
