@@ -233,20 +233,30 @@ __device__ __forceinline__ void finish_mma(uint64_t *done) {
 // Rows of a ring's tile that are summed over but belong to something else are set to
 // zero by a warp of its own, at the request of the (single) MMA thread, which has seen
 // the tile arrive and waits for `clean` before the product that reads it.  job: the
-// stage (-1: no more requests) and the first row; one request at a time.
+// stage (-1: no more requests), the first row, and the MMA thread's steps so far; one
+// request at a time.
 __device__ __forceinline__ void request_clear(uint64_t *req, volatile int *job, int stage, int row) {
     job[0] = stage;
     job[1] = row;
     mbar_arrive(req);
 }
 __device__ __forceinline__ void clear_role(uint8_t *ring, int tile_bytes, int halves, uint64_t *req, uint64_t *clean,
-                                           volatile int *job, volatile int *abort, int lane) {
-    const uint64_t t0 = globaltimer();
+                                           volatile int *job, volatile int *abort, uint64_t limit_ns, int lane) {
+    // Requests may be any time apart.  The MMA thread ends with a request or with the abort flag
+    // set, and between two of its steps are at most 15 waits of limit_ns: while it makes steps
+    // the role stays, and 32 such waits without one are the bound.
+    const uint64_t idle_ns = limit_ns < (1ull << 58) ? 32 * limit_ns : 1ull << 63;
+    uint64_t t0 = globaltimer();
+    int steps = 0;
     for (int n = 0;; ++n) {
-        // requests may be far apart: bounded by the life of the kernel (the MMA thread's waits
-        // are bounded, and it ends with a request or with the abort flag set), and by a minute
-        while (!__all_sync(0xffffffffu, mbar_try(req, n & 1)))
-            if (__any_sync(0xffffffffu, *abort != 0 || globaltimer() - t0 > 60000000000ull)) return;
+        while (!__all_sync(0xffffffffu, mbar_try(req, n & 1))) {
+            const int s = job[2];
+            if (s != steps) {
+                steps = s;
+                t0 = globaltimer();
+            }
+            if (__any_sync(0xffffffffu, *abort != 0 || globaltimer() - t0 > idle_ns)) return;
+        }
         const int stage = job[0], row = job[1];
         if (stage < 0) return;
         uint8_t *tile = ring + stage * tile_bytes;

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
     uint64_t *done = bar + 15, *clean = bar + 16, *clear_req = bar + 17, *p_half = bar + 10, *ring_full = bar + kBarriers, *ring_empty = ring_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
-    volatile int *clear_job = abort_flag + 1;  // stage, first row
+    volatile int *clear_job = abort_flag + 1;  // stage, first row, steps
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int tt = 128 / a.G, rows = tt * a.G;
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
         mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
         *abort_flag = 0;
+        clear_job[2] = 0;
         mbar_fence_init();
     }
     // rows that no box writes (G does not divide 128) take part in the sums over rows: zeros
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
             auto wait1 = [&](uint64_t *x, uint32_t par) { return thread_wait(x, par & 1, wait_ns, abort_flag, a.ds, 12); };
             const uint32_t kb = smem_u32(sm + L::OFF_FIX), vb = kb + L::TILE;
             Ring<L::ST> ring;
-            int np = 0, nc = 0;
+            int np = 0, nc = 0;  // np: steps
             bool ok = true;
             for (int n = 0; ok; ++n) {
                 const int ib = n % kItems;
@@ -296,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
                 mma_commit(dp_full);
                 for (int j = j0; j < j1; ++j) {
                     const bool more = j + 1 < j1;
+                    clear_job[2] = np + 1;
                     auto next_scores = [&]() -> bool {
                         if (!take(j + 1, qn)) return false;
                         tc_fence_after();
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_key_tc_kernel(
         }
         __syncwarp();
     } else if (warp == kWarpClear) {
-        clear_role(sm + L::OFF_RING, L::TILE, L::NH, clear_req, clean, clear_job, abort_flag, lane);
+        clear_role(sm + L::OFF_RING, L::TILE, L::NH, clear_req, clean, clear_job, abort_flag, wait_ns, lane);
     } else if (warp == kWarpStat) {
         // ============================================================ row statistics of each tile
         int nt = 0;
@@ -485,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
     uint64_t *done = bar + 12, *clean = bar + 13, *clear_req = bar + 14, *join = bar + 15, *out_read = bar + 16, *ring_full = bar + kBarriers, *ring_empty = ring_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
-    volatile int *clear_job = abort_flag + 1;  // stage, first row
+    volatile int *clear_job = abort_flag + 1;  // stage, first row, steps
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int tt = 128 / a.G, rows = tt * a.G;
@@ -497,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
         mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&ring_full[i], 1); mbar_init(&ring_empty[i], 1); }
         *abort_flag = 0;
+        clear_job[2] = 0;
         mbar_fence_init();
     }
     if (warp == kWarpMma) {
@@ -634,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
                     mbar_arrive(&ring_empty[out.st]);
                 }
                 for (int j = 0; ok && j < nn; ++j) {
+                    clear_job[2] = nt + j + 1;
                     // (S of step j + 1 goes over that of j - 1: read, and its dS multiplied, before dP of j)
                     if (j + 1 < nn) {
                         if (!(ok = scores(j + 1, kn) && dprob(j + 1))) break;
@@ -658,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_row_tc_kernel(
         }
         __syncwarp();
     } else if (warp == kWarpClear) {
-        clear_role(sm + L::OFF_RING, L::TILE, L::NH, clear_req, clean, clear_job, abort_flag, lane);
+        clear_role(sm + L::OFF_RING, L::TILE, L::NH, clear_req, clean, clear_job, abort_flag, wait_ns, lane);
     } else if (warp < 8) {
         // ============================================================ dS, 64 keys per warpgroup
         const int w = warp >> 2, r = threadIdx.x & 127;

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
     uint64_t *kv_full = done + 1, *kv_empty = kv_full + L::ST;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::OFF_MISC + 16);
-    volatile int *clear_job = abort_flag + 1;  // stage, first row
+    volatile int *clear_job = abort_flag + 1;  // stage, first row, steps
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
         mbar_init(done, 1); mbar_init(clean, 1); mbar_init(clear_req, 1);
         for (int i = 0; i < L::ST; ++i) { mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1); }
         *abort_flag = 0;
+        clear_job[2] = 0;
         mbar_fence_init();
     }
     if (warp == kWarpMma) {
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             if (elect_one()) {
                 auto wait1 = [&](uint64_t *b, uint32_t par) { return thread_wait(b, par & 1, wait_ns, abort_flag, a.ds, 2); };
                 Ring<L::ST> kv;
-                int nq[2] = {0, 0}, np[2] = {0, 0}, nc = 0;
+                int nq[2] = {0, 0}, np[2] = {0, 0}, nc = 0, steps = 0;
                 bool ok = true;
                 for (int n = 0; ok; ++n) {
                     const int ib = n % kItems;
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
                         if ((s ? n1 : n0) == 1) mma_commit(&q_empty[s]);
                     }
                     for (int j = 0; ok && j < nn; ++j) {
+                        clear_job[2] = ++steps;
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
                             const int ns = s ? n1 : n0;
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(
             __syncwarp();
         } else if (warp == kWarpClear) {
             // ======================================================== values behind the last key
-            clear_role(sm + L::OFF_KV, L::TILE, L::NH, clear_req, clean, clear_job, abort_flag, lane);
+            clear_role(sm + L::OFF_KV, L::TILE, L::NH, clear_req, clean, clear_job, abort_flag, wait_ns, lane);
         }
     } else {
         // ============================================================ softmax, one warpgroup per stream

@@ -108,3 +108,63 @@ def test_loads_and_products_are_awaited_whoever_gave_up(file):
     loads = len(re.findall(r"mbar_arrive_expect_tx\(", src))
     assert len(re.findall(r"\bland\(", src)) == loads
     assert len(re.findall(r"\bfinish_mma\(", src)) == len(re.findall(r"tmem_alloc\(", src))
+
+
+# Requests at the given times, then (at `last`) the final one; the MMA thread makes a step every `step` ns.
+CLEAR = r"""
+static volatile int job[3], gave_up;
+static uint64_t step, last = 0;  // (0: no final request)
+static bool step_try(uint64_t *b, uint32_t parity) {
+    const bool done = mbar_try(b, parity);
+    job[2] = step ? (int)(now / step) : 0;
+    job[0] = last && now >= last ? -1 : 1;
+    return done;
+}
+#define mbar_try step_try
+%s
+#undef mbar_try
+static int serve(std::vector<uint64_t> when, int row, uint8_t *ring) {  // requests answered; stops at the end or when it gives up
+    model[0].when = when;
+    if (last) model[0].when.push_back(last);
+    int answered = -1;
+    for (int lane = 0; lane < 32; ++lane) {
+        now = 0; tick = 1000000;
+        model[1].arrived = 0;
+        job[1] = row; job[2] = 0;
+        clear_role(ring, 32768, 2, bars, bars + 1, job, &gave_up, 2000000000ull, lane);
+        if (lane == 0) answered = model[1].arrived;
+    }
+    return answered;
+}
+int main() { %s }"""
+
+
+def test_the_clearing_role_outlasts_a_long_kernel(tmp_path):
+    """Requests a minute and more after the kernel began, and as far apart, are answered."""
+    out = run_host(tmp_path, CLEAR % (function("clear_role"), """
+    static uint8_t ring[2 * 32768];
+    memset(ring, 7, sizeof ring);
+    step = 1000000000;
+    last = 300000000000ull;
+    printf("%d ", serve({61000000000ull, 200000000000ull}, 50, ring));
+    int cleared = 0, kept = 0;
+    for (int h = 0; h < 2; ++h)
+        for (int r = 0; r < 128; ++r)
+            for (int c = 0; c < 128; ++c) (r < 50 ? kept : cleared) += ring[32768 + h * 16384 + r * 128 + c] == (r < 50 ? 7 : 0);
+    for (int i = 0; i < 32768; ++i) kept += ring[i] == 7;
+    printf("%d %d\\n", cleared, kept);"""))
+    assert out == ["2", str(2 * 78 * 128), str(2 * 50 * 128 + 32768)]
+
+
+def test_the_clearing_role_leaves(tmp_path):
+    """When the MMA thread makes no step for long; at once when another role gave up."""
+    out = run_host(tmp_path, CLEAR % (function("clear_role"), """
+    static uint8_t ring[2 * 32768];
+    step = 0;
+    printf("%d ", serve({}, 50, ring));
+    printf("%llu ", (ull)(now / 1000000000));
+    step = 1000000000;
+    gave_up = 1;
+    printf("%d ", serve({}, 50, ring));
+    printf("%d\\n", now < 10000000);"""))
+    assert out[0] == "0" and 30 < int(out[1]) < 100 and out[2:] == ["0", "1"]
