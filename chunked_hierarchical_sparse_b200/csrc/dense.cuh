@@ -14,6 +14,7 @@
 namespace hsa {
 namespace dense {
 
+constexpr int32_t kKDense = 12;  // DevStatus::where of these kernels (KernelId goes to 11)
 constexpr int kSimtRows = 64;    // rows and keys of a CUDA-core tile
 constexpr int kNoMask = 0x3fffffff;  // causal offset of an item whose keys are all visible
 

@@ -27,8 +27,7 @@ struct DevStatus {
 
 enum KernelId : int32_t {
     kKPool = 1, kKSelect = 2, kKAttendSimt = 3, kKDecode = 4, kKBwd1 = 5, kKInvert = 6,
-    kKBwd2 = 7, kKAttendTc = 8, kKFinal = 9, kKSelectTc = 10, kKBwdTc = 11,
-    kKDense = 12
+    kKBwd2 = 7, kKAttendTc = 8, kKFinal = 9, kKSelectTc = 10, kKBwdTc = 11
 };
 
 __device__ __forceinline__ void report(DevStatus *st, int32_t code, int32_t where, int32_t a,
