@@ -364,16 +364,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(
         }
         if (!ok) {
             *abort_flag = 1;
-            if (lane == 0) {
-                report(ds, HSA_ERR_TIMEOUT, kKAttendTc, 2, it);
-                // let the loads already issued land before the CTA goes away (bounded)
-                for (int s2 = 0; s2 < kQStages; ++s2) {
-                    if (qc > s2) mbar_wait(&B.q_full[(qc - 1 - s2) % kQStages], ((qc - 1 - s2) / kQStages) & 1, kDrainWaitNs);
-                    if (s2 < 2 && kvc > s2) mbar_wait(&B.kv_full[(kvc - 1 - s2) & 1], ((kvc - 1 - s2) >> 1) & 1, kDrainWaitNs);
-                }
-            }
-            __syncwarp();
+            if (lane == 0) report(ds, HSA_ERR_TIMEOUT, kKAttendTc, 2, it);
         }
+        // the loads already issued land before the CTA goes away (bounded), whichever role gave up
+        if (lane == 0) {
+            for (int s2 = 0; s2 < kQStages; ++s2) {
+                if (qc > s2) mbar_wait(&B.q_full[(qc - 1 - s2) % kQStages], ((qc - 1 - s2) / kQStages) & 1, kDrainWaitNs);
+                if (s2 < 2 && kvc > s2) mbar_wait(&B.kv_full[(kvc - 1 - s2) & 1], ((kvc - 1 - s2) >> 1) & 1, kDrainWaitNs);
+            }
+        }
+        __syncwarp();
     } else if (warp == kWarpMma) {
         // ============================================================ MMA issuer
         // Two in-order streams polled by one lane: S(t) = Q_t K^T is issued as

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kBThreads, 1) bwd_tc_kernel(
         // Units (whole (window, chunk) buckets) are dealt to the CTAs in queue
         // order; descriptors are loaded one unit ahead and each tile's entries
         // and weights one tile ahead.
-        int it = 0, qc = 0, useq = 0;
+        int it = 0, qc = 0, useq = 0, kvc = 0;  // kvc: K/V loads issued
         bool ok = true;
         const int total = min(P.seg_start[P.J], P.max_items);
         const int qstep = gridDim.x;
@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kBThreads, 1) bwd_tc_kernel(
                     tma_load_2d(sm + L::OFF_V + h * L::KVHALF, &tm_v, h * 64, row, kv_full);
                 }
             }
+            ++kvc;
             for (int tt = t0; tt < t1 && ok; ++tt) {
                 const Pay pn = (tt + 1 < t1) ? tile_pay(dc, tt + 1) : tile_pay(dn, dn.b.y);
                 const int ii = it % kBInfo;
@@ -345,15 +346,15 @@ __global__ void __launch_bounds__(kBThreads, 1) bwd_tc_kernel(
         }
         if (!ok) {
             *abort_flag = 1;
-            if (lane == 0) {
-                report(ds, HSA_ERR_TIMEOUT, kKBwdTc, 2, it);
-                // let the loads already issued land before the CTA goes away (bounded)
-                for (int s2 = 0; s2 < 2; ++s2)
-                    if (qc > s2) mbar_wait(&qd_full[(qc - 1 - s2) & 1], ((qc - 1 - s2) >> 1) & 1, kDrainWaitNs);
-                if (useq > 0) mbar_wait(kv_full, (useq - 1) & 1, kDrainWaitNs);
-            }
-            __syncwarp();
+            if (lane == 0) report(ds, HSA_ERR_TIMEOUT, kKBwdTc, 2, it);
         }
+        // the loads already issued land before the CTA goes away (bounded), whichever role gave up
+        if (lane == 0) {
+            for (int s2 = 0; s2 < 2; ++s2)
+                if (qc > s2) mbar_wait(&qd_full[(qc - 1 - s2) & 1], ((qc - 1 - s2) >> 1) & 1, kDrainWaitNs);
+            if (kvc > 0) mbar_wait(kv_full, (kvc - 1) & 1, kDrainWaitNs);
+        }
+        __syncwarp();
     } else if (warp == kBWarpMma) {
         // ============================================================ MMA issuer
         // Two in-order streams polled by one lane:

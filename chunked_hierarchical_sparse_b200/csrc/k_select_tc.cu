@@ -200,9 +200,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_tc_kernel(
             issued = i + 1;
             __syncwarp();
         }
-        if (!ok && lane == 0) {
-            report(ds, HSA_ERR_TIMEOUT, kKSelectTc, 1, t0);
-            // let the loads already issued land before the CTA can go away (bounded)
+        if (!ok && lane == 0) report(ds, HSA_ERR_TIMEOUT, kKSelectTc, 1, t0);
+        // the loads already issued land before the CTA goes away (bounded), whichever role gave up
+        if (lane == 0) {
+            if (ntiles > 0) mbar_wait(q_full, 0, kDrainWaitNs);
             for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait(&b_full[i & 1], (i >> 1) & 1, kDrainWaitNs);
         }
     } else if (warp == 1) {

@@ -38,3 +38,34 @@ def test_waits_that_run_out_with_every_load_issued(L, G, d):
         assert codes == [5, 5, 5]
         again, gd2 = run_prompt(x), run_decode(dx)
         assert all(torch.equal(good[n], again[n]) for n in good) and torch.equal(gd["o"], gd2["o"])
+
+
+@pytest.mark.parametrize("L,G,d", [(200, 16, 64), (330, 8, 128), (700, 8, 64)])
+def test_sparse_waits_that_run_out_with_few_loads(L, G, d):
+    """The same for the sparse forward and backward beside them."""
+    m = hsa()
+    K = 4
+    x = inputs(1, L, 2 * G, 2, d, "bf16", seed=L)
+    qs = x["q"][:, :, ::G].contiguous()
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    good = m.hsa_fwd(x["q"], x["k"], x["v"], qs, K)
+    gb = m.hsa_bwd(x["q"], x["k"], x["v"], qs, x["dO"], *good[1:], K)
+    for _ in range(10):
+        m.hsa_set_wait_limit_ns(1)
+        try:
+            m.hsa_fwd(x["q"], x["k"], x["v"], qs, K, ws=ws)
+            codes = [m.hsa_device_status(ws)]
+            m.hsa_bwd(x["q"], x["k"], x["v"], qs, x["dO"], *good[1:], K, ws=ws)
+            codes.append(m.hsa_device_status(ws))
+        finally:
+            m.hsa_set_wait_limit_ns(0)
+        assert 5 in codes and all(c in (0, 5) for c in codes)
+        again = m.hsa_fwd(x["q"], x["k"], x["v"], qs, K, ws=ws)
+        assert m.hsa_device_status(ws) == 0
+        # its fp16 sums may be taken in another order: one half-step of fp16 per term, K terms
+        assert float((again[0].float() - good[0].float()).abs().max()) <= K * 2 ** -8 * float(good[0].abs().max())
+        assert torch.equal(again[2], good[2])
+        bb = m.hsa_bwd(x["q"], x["k"], x["v"], qs, x["dO"], *good[1:], K, ws=ws)
+        assert m.hsa_device_status(ws) == 0
+        for a, b in zip(bb, gb):
+            assert float((a.float() - b.float()).norm()) <= 2 ** -7 * float(b.float().norm())

@@ -110,6 +110,27 @@ def test_loads_and_products_are_awaited_whoever_gave_up(file):
     assert len(re.findall(r"\bfinish_mma\(", src)) == len(re.findall(r"tmem_alloc\(", src))
 
 
+@pytest.mark.parametrize("file,bars", [("k_attend_tc.cu", ["B.q_full[", "B.kv_full[", "mma_done"]),
+                                       ("k_bwd_tc.cu", ["qd_full[", "kv_full,", "mma_done"]),
+                                       ("k_select_tc.cu", ["q_full", "b_full[", "mma_done"])])
+def test_the_sparse_kernels_await_their_loads_too(file, bars):
+    """Each barrier that a copy or a product completes is awaited at the end, outside of any `if (!ok)`."""
+    src = source(file)
+    for bar in bars:
+        at = [m.start() for m in re.finditer(r"mbar_wait\(&?" + re.escape(bar) + r"[^;]*kDrainWaitNs", src)]
+        assert len(at) == 1, bar
+        # the blocks that enclose the wait, innermost first
+        depth, i, heads = 0, at[0], []
+        while i > 0 and len(heads) < 4:
+            i -= 1
+            depth += {"}": 1, "{": -1}.get(src[i], 0)
+            if depth < 0:
+                heads.append(src[src.rindex("\n", 0, i) + 1:i].strip())
+                depth = 0
+        line = src[src.rindex("\n", 0, at[0]) + 1:at[0]]
+        assert not any("!ok" in h for h in heads + [line]), (bar, heads)
+
+
 # Requests at the given times, then (at `last`) the final one; the MMA thread makes a step every `step` ns.
 CLEAR = r"""
 static volatile int job[3], gave_up;
