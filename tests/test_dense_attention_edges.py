@@ -69,3 +69,22 @@ def test_sparse_waits_that_run_out_with_few_loads(L, G, d):
         assert m.hsa_device_status(ws) == 0
         for a, b in zip(bb, gb):
             assert float((a.float() - b.float()).norm()) <= 2 ** -7 * float(b.float().norm())
+
+
+# ------------------------------------------------------------ bad values at the edges of tiles
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("G", [1, 3, 5, 6, 7, 8, 12, 16])
+def test_a_bad_value_reaches_no_further_back_than_documented(G, dtype):
+    """NaN in v at the last token of a tile of 128 keys, and one before and behind it: the rows more
+    than 127 tokens before it (126 + floor(128 / G) where G does not divide 128) keep their bits."""
+    m = hsa()
+    x = inputs(1, 700, 2 * G, 2, 64, dtype, seed=G)
+    good = m.hsa_prompt_fwd(x["q"], x["k"], x["v"])[0]
+    reach = 127 if 128 % G == 0 else 126 + 128 // G
+    for t in (254, 255, 256, 383, 511, 639, 699):
+        v = x["v"].clone()
+        v[0, 1, t] = np.nan
+        o, lse = m.hsa_prompt_fwd(x["q"], x["k"], v)
+        assert torch.equal(o[:, :, :G], good[:, :, :G])  # the other group
+        assert torch.equal(o[:, :max(0, t - reach)], good[:, :max(0, t - reach)]), t
+        assert torch.isnan(o[:, t:, G:]).all() and torch.isfinite(lse).all()
