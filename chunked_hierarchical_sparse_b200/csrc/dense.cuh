@@ -282,7 +282,7 @@ cudaError_t launch_bwd_tc(const BwdArgs &b, int d, int64_t row_items, int64_t ke
 cudaError_t launch_cache(const Args &a, int d, bool first, cudaStream_t st);
 cudaError_t launch_combine(const Args &a, int d, bool bf16, cudaStream_t st);
 cudaError_t launch_add_pieces(const BwdArgs &b, int d, cudaStream_t st);
-cudaError_t launch_delta(const BwdArgs &b, int d, cudaStream_t st);  // fp32
+cudaError_t launch_delta(const BwdArgs &b, int d, const int32_t *cu, int n_seq, cudaStream_t st);  // fp32
 cudaError_t launch_bwd_simt(const BwdArgs &b, int d, int64_t row_items, int64_t key_items, cudaStream_t st);
 
 }  // namespace dense

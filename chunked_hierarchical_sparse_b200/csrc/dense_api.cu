@@ -298,7 +298,7 @@ hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, cons
         else
             e = launch_plan(keys, nullptr, b.a.ds, st);
     }
-    if (e == cudaSuccess && !tc) e = launch_delta(b, shape->d, st);
+    if (e == cudaSuccess && !tc) e = launch_delta(b, shape->d, cu_seqlens, shape->n_seq, st);
     if (e == cudaSuccess) {
         const int64_t rows = row_items(*shape, b.a.tok), keys = row_items(*shape, key_tile(*shape)) + (w.part ? kMaxPieces : 0);
         e = tc ? launch_bwd_tc(b, shape->d, rows, keys, word(ws, kWordNext), st)

@@ -251,15 +251,18 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) fwd_simt_kernel(const _
     cl.sync();  // no block leaves while another reads its memory
 }
 
-// delta[row] = dO . o, one warp per (token, head) row; `header`: to be cleared (null: by a kernel before)
+// delta[row] = dO . o, one warp per (token, head) row; `header`: to be cleared (null: by a kernel before).
+// Packed (`cu`; the plan has looked at it, and has no items where it does not rise): the sequences' rows only.
 template <int D>
-__global__ void __launch_bounds__(256) delta_kernel(const float *o, const float *dO, float *delta, int64_t rows, DevStatus *header) {
+__global__ void __launch_bounds__(256) delta_kernel(const float *o, const float *dO, float *delta, int64_t rows, DevStatus *header,
+                                                    const int32_t *cu, int n_seq, int hq, const int32_t *plan_n) {
     const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     dependency_wait();
     dependents_may_start();
     if (header && blockIdx.x == 0) clear_header(header);
     if (r >= rows) return;
+    if (cu && (*plan_n == 0 || r < (int64_t)cu[0] * hq || r >= (int64_t)cu[n_seq] * hq)) return;
     float s = 0.f;
 #pragma unroll
     for (int c = 0; c < D; c += 128) {
@@ -540,10 +543,11 @@ template <int D> cudaError_t fwd(const Args &a, int64_t items, cudaStream_t st) 
     return launch_next(a.plan != nullptr, fwd_simt_kernel<D>, (int)items * c, kThr, fwd_smem<D>(), st, c, a);
 }
 
-template <int D> cudaError_t delta(const BwdArgs &b, cudaStream_t st) {
+template <int D> cudaError_t delta(const BwdArgs &b, const int32_t *cu, int n_seq, cudaStream_t st) {
     const int64_t rows = (int64_t)b.a.B * b.a.L * b.a.hq;
     return launch_next(b.a.plan != nullptr, delta_kernel<D>, (int)ceil_div(rows, 8), 256, 0, st, 1,
-                       static_cast<const float *>(b.o), static_cast<const float *>(b.dO), b.delta, rows, b.a.plan ? nullptr : b.a.ds);
+                       static_cast<const float *>(b.o), static_cast<const float *>(b.dO), b.delta, rows, b.a.plan ? nullptr : b.a.ds,
+                       cu, n_seq, b.a.hq, b.a.plan_n);
 }
 
 template <int D> cudaError_t bwd(const BwdArgs &b, int64_t row_items, int64_t key_items, cudaStream_t st) {
@@ -562,8 +566,8 @@ cudaError_t launch_fwd_simt(const Args &a, int d, int64_t items, cudaStream_t st
     return d == 128 ? fwd<128>(a, items, st) : fwd<64>(a, items, st);
 }
 
-cudaError_t launch_delta(const BwdArgs &b, int d, cudaStream_t st) {
-    return d == 128 ? delta<128>(b, st) : delta<64>(b, st);
+cudaError_t launch_delta(const BwdArgs &b, int d, const int32_t *cu, int n_seq, cudaStream_t st) {
+    return d == 128 ? delta<128>(b, cu, n_seq, st) : delta<64>(b, cu, n_seq, st);
 }
 
 cudaError_t launch_bwd_simt(const BwdArgs &b, int d, int64_t row_items, int64_t key_items, cudaStream_t st) {

@@ -236,7 +236,7 @@ HSA_API size_t hsa_prompt_workspace_size(const hsa_prompt_shape_t *shape, int op
  * with n_seq = 0): sequence s is the tokens cu_seqlens[s] .. cu_seqlens[s+1]-1;
  * it must rise (equal neighbours: an empty sequence) within [0, L], otherwise
  * HSA_ERR_DEVICE_CHECK is reported and nothing is written.  Rows outside every
- * sequence are neither read nor written.  A NaN or infinity in q, k or v at
+ * sequence are not written, and what they hold has no influence.  A NaN or infinity in q, k or v at
  * token t reaches the rows of its own sequence only; in v at token t also rows
  * before it may become NaN (masked weights are zeros of a matrix product): up to
  * 127 tokens before it, or, where G = h_q / h_kv does not divide 128 and row
@@ -250,8 +250,8 @@ HSA_API hsa_status_t hsa_prompt_fwd(const hsa_prompt_shape_t *shape, const void 
 
 /* Backward of hsa_prompt_fwd: gradients of sum(dO * o), from its inputs and its
  * o and lse (which carry off_by_one).  dq [B,L,h_q,d], dk, dv [B,h_kv,L,d], all
- * required; rows outside every sequence are neither read nor written.  A NaN or
- * infinity at a token reaches gradients of its own sequence only. */
+ * required; rows outside every sequence as in the forward.  A NaN or infinity at a
+ * token reaches gradients of its own sequence only. */
 HSA_API hsa_status_t hsa_prompt_bwd(const hsa_prompt_shape_t *shape, const void *q, const void *k,
                                     const void *v, const void *o, const void *dO, const float *lse,
                                     const int32_t *cu_seqlens, void *dq, void *dk, void *dv, void *ws,

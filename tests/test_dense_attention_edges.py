@@ -88,3 +88,22 @@ def test_a_bad_value_reaches_no_further_back_than_documented(G, dtype):
         assert torch.equal(o[:, :, :G], good[:, :, :G])  # the other group
         assert torch.equal(o[:, :max(0, t - reach)], good[:, :max(0, t - reach)]), t
         assert torch.isnan(o[:, t:, G:]).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("lens", [[40, 0, 61], [0, 0]])
+def test_fp32_backward_leaves_rows_outside_every_prompt_alone(lens):
+    """Nothing of the rows before the first and behind the last prompt reaches even the workspace."""
+    m = hsa()
+    L = 5 + sum(lens) + 7
+    x = inputs(1, L, 6, 2, 64, "fp32", seed=50)
+    cu = cu_of(lens, 5)
+    b = run_prompt(x, cu)
+    outside = np.r_[0:5, L - 7:L]
+    o, dO, lse = b["o"], x["dO"], b["lse"]
+    for t in (o, dO, lse):
+        t[:, outside] = np.nan
+    ws = torch.full((m.hsa_prompt_workspace_size(1, L, 6, 2, 64, torch.float32, m.OP_BWD, len(lens)) // 4,), 1.0, device=DEV)
+    g = m.hsa_prompt_bwd(x["q"], x["k"], x["v"], o, dO, lse, cu, dq=b["dq"].clone(), dk=b["dk"].clone(), dv=b["dv"].clone(), ws=ws)
+    assert m.hsa_device_status(ws) == 0
+    assert all(torch.equal(a, b[n]) for a, n in zip(g, ("dq", "dk", "dv")))
+    assert not torch.isnan(ws).any()
