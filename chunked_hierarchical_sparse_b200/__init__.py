@@ -144,6 +144,8 @@ def _run(name: str, dev, stream, *args):
     """Call a C entry point with the tensors' device current, on the given stream or
     else that device's current stream (the library launches on the current device)."""
     fn = getattr(load_library(), name)
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: the tensors must be on a GPU, not on {dev}")
     if stream is None:
         s = torch._C._cuda_getCurrentRawStream(dev.index)  # current_stream(dev), without its wrapper object
     elif stream.device != dev:
