@@ -410,7 +410,12 @@ def hsa_prompt_fwd(q, k, v, cu_seqlens=None, off_by_one: bool = False, want_lse:
     """Causal attention over whole prompts.  q [B,L,h_q,d], k, v [B,h_kv,L,d]; each batch
     row is one prompt, or (B = 1) cu_seqlens (int32, on the GPU) gives the bounds of the
     prompts packed into it.  Returns (o, lse); rows outside every prompt keep what o and
-    lse held (a tensor that the call allocates is not initialised there)."""
+    lse held (a tensor that the call allocates is not initialised there).
+
+    The bounds are looked at on the GPU.  Where they do not rise within [0, L], nothing is
+    written, so o and lse keep what they held (as above), and the report stands in the
+    workspace alone: to learn of it, pass `ws` (hsa_prompt_workspace_size bytes) and read
+    it with hsa_device_status(ws)."""
     if stream is not None:
         with _allocating(q.device, stream):
             return hsa_prompt_fwd(q, k, v, cu_seqlens, off_by_one, want_lse, o, lse, ws)
@@ -428,7 +433,8 @@ def hsa_prompt_fwd(q, k, v, cu_seqlens=None, off_by_one: bool = False, want_lse:
 
 def hsa_prompt_bwd(q, k, v, o, dO, lse, cu_seqlens=None, dq=None, dk=None, dv=None, ws=None, stream=None):
     """Backward of hsa_prompt_fwd (o and lse as it returned them, with or without
-    off_by_one).  Returns (dq, dk, dv); rows outside every prompt as in the forward."""
+    off_by_one).  Returns (dq, dk, dv); rows outside every prompt, and bounds that do not
+    rise, as in the forward."""
     if stream is not None:
         with _allocating(q.device, stream):
             return hsa_prompt_bwd(q, k, v, o, dO, lse, cu_seqlens, dq, dk, dv, ws)
@@ -473,7 +479,8 @@ def hsa_prefix_decode(q, k_prefix, v_prefix, k_cache, v_cache, lens, off_by_one:
     """One decode step of sequences that share their first P tokens.  q [B,h_q,d];
     k_prefix, v_prefix [h_kv,P,d] (for example the first P tokens of one prompt's k[0],
     v[0] in hsa_prompt_fwd); k_cache, v_cache [B,h_kv,cap,d] with the lens[b] (int32, on
-    the GPU) tokens that sequence b has of its own.  Returns (o, lse)."""
+    the GPU) tokens that sequence b has of its own; a length outside [0, cap] is taken as the
+    nearest bound and reported in the workspace (`ws`, hsa_device_status).  Returns (o, lse)."""
     if stream is not None:
         with _allocating(q.device, stream):
             return hsa_prefix_decode(q, k_prefix, v_prefix, k_cache, v_cache, lens, off_by_one, want_lse, o, lse, ws)
