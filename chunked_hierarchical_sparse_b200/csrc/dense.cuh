@@ -191,8 +191,9 @@ struct PlanJob {
 // A key tile whose rows are more than an SM's share of `work` steps (and an eighth, so that
 // a last round of whole tiles is not cut for nothing) is cut into pieces of at most
 // key_limit row tiles: two thirds of an SM's share, but worth their partials (4 steps).
-// (Backward of one prompt of 4K and 8K tokens, 16 heads in 2 groups: 258 and 846 us;
-// pieces of a whole share 287 and 924, of half of one 279 and 904; uncut 562 and 1262.)
+// (Backward of one prompt of 2K, 4K and 8K tokens, 16 heads in 2 groups, d = 128: 91, 229 and
+// 777 us; pieces of a whole share 91, 247 and 851, of half of one 87, 237 and 836; uncut 233,
+// 480 and 1188.)
 // A cut tile has fewer than 2 rows / limit pieces, so all cut tiles together have fewer
 // than 3 kPlanSms: the number of partial slots is bounded whatever the lengths are.
 __host__ __device__ __forceinline__ int key_limit(unsigned long long work) {

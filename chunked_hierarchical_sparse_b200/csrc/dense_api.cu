@@ -197,10 +197,15 @@ PrefixPlan plan_prefix(const hsa_prefix_shape_t &s) {
     p.pre_tiles = (int)ceil_div(s.B, p.tok);
     if (tc) {
         // The prefix: one item per SM, of two tiles of 128 keys at least (a second round of
-        // items costs more than it balances: 256 x 32K tokens 80 us, 96 with two rounds).  Where
-        // it keeps every SM for long (8 steps of 256 x 128 and more), it leaves to the own caches,
-        // which are bound by HBM, as many SMs as let them finish beside it: a step takes about
-        // 1.8 us (d = 128), an SM reads about 110 GB/s, and half of cap is taken as used.
+        // items costs more than it balances: 256 sequences behind 32K tokens with up to 2K of
+        // their own 107 us, 124 with two rounds).  Where it keeps every SM for long (8 steps of
+        // 256 x 128 and more), it leaves to the own caches, which are bound by HBM, as many SMs
+        // as let them finish beside it: a step takes about 1.8 us (d = 128), an SM reads about
+        // 110 GB/s, and half of cap is taken as used, since the lengths are on the device.  That
+        // step without the SMs left free: 123 us; every cache full 149, 167 without; 128 sequences
+        // with up to 8K tokens of their own 112, 135 without.  Where the caches are all but empty
+        // the SMs are left free for nothing: up to 32 tokens in a cap of 2K 90 us, 81 without, up
+        // to 64 in a cap of 8K 67, 47 without.
         const int64_t jobs = (int64_t)s.h_kv * p.pre_tiles;
         const double steps = (double)jobs * (p.split ? 0.5 : 1.0) * ceil_div(s.P, 128);
         const double pre_us = steps * 1.8 * s.d / 128, suf_us = 0.5 * s.B * s.h_kv * (double)s.cap * 4 * s.d / 110e3;
@@ -208,7 +213,8 @@ PrefixPlan plan_prefix(const hsa_prefix_shape_t &s) {
         if (steps >= 8 * kSms) sms -= (int)std::min(kSms * suf_us / (pre_us + suf_us), kSms / 2.0);
         p.pre_sub = slot_keys(s.P, jobs, sms, 256);
         // The own caches: three blocks fit an SM, ragged lengths want several rounds of them (the
-        // step above with ranges of 2048, 1024 and 512 keys: 114, 106, 110 us).
+        // first step above with ranges of 2048, 1024 and 512 keys: 112, 107, 111 us; with every
+        // cache full 142, 149, 152).
         p.suf_sub = slot_keys(s.cap, (int64_t)s.h_kv * s.B, 8 * kSms, 256);
     } else {  // about two blocks of 64-key tiles per SM
         p.pre_sub = slot_keys(s.P, (int64_t)s.h_kv * p.pre_tiles, 2 * kSms, kSimtRows);

@@ -6,7 +6,9 @@
 // pass over the keys; o = O / l, lse = (m + log2 l) ln 2.  m is a running
 // maximum that is only moved (and O, l rescaled) when a tile exceeds it by more
 // than 2^8: p then stays below 256, which neither fp32 sums nor bf16 operands
-// mind, and O in tensor memory is almost never touched.
+// mind, and O in tensor memory is almost never touched.  (The online softmax of Milakov
+// and Gimelshein, 2018; a maximum moved only beyond a bound, two row tiles in turns and P
+// over S in tensor memory are published steps of attention on this generation of GPUs.)
 //
 // One persistent CTA per SM with two streams, each a 128-row tile with its own S
 // and O in tensor memory and its own softmax warpgroup (one thread per row, the
