@@ -314,7 +314,7 @@ HSA_API hsa_status_t hsa_device_status(const void *ws, int32_t *code_out, void *
 
 /* Testing aid for the failure path.  Every wait inside the library's persistent
  * kernels (the chunk-major attention, the tensor-core selection and the
- * tensor-core backward) is bounded by `ns` nanoseconds of wall-clock time; 0
+ * tensor-core backward; the dense attention in bf16) is bounded by `ns` nanoseconds of wall-clock time; 0
  * restores the default bound of 2 s.  A wait that runs out makes the kernel
  * record HSA_ERR_TIMEOUT in the status word, stop its work, let the copies and
  * MMAs it has issued finish (these waits keep the 2 s bound), free its tensor
