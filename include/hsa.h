@@ -236,14 +236,14 @@ HSA_API size_t hsa_prompt_workspace_size(const hsa_prompt_shape_t *shape, int op
  * with n_seq = 0): sequence s is the tokens cu_seqlens[s] .. cu_seqlens[s+1]-1;
  * it must rise (equal neighbours: an empty sequence) within [0, L], otherwise
  * HSA_ERR_DEVICE_CHECK is reported and nothing is written.  Rows outside every
- * sequence are not written, and what they hold has no influence.  A NaN or infinity in q, k or v at
- * token t reaches the rows of its own sequence only; in v at token t also rows
- * before it may become NaN (masked weights are zeros of a matrix product): up to
- * 127 tokens before it, or, where G = h_q / h_kv does not divide 128 and row
- * tiles of floor(128 / G) tokens reach across the tiles of 128 keys, up to
- * 126 + floor(128 / G).  So what stands in v behind a batch row's last token of
- * interest (padding) has to be finite, or the prompts packed by cu_seqlens, where
- * everything behind a sequence is kept out. */
+ * sequence are not written, and what they hold has no influence.  A NaN or
+ * infinity in q, k or v at token t reaches the rows of its own sequence only; in
+ * v at token t also rows before it may become NaN (masked weights are zeros of a
+ * matrix product): up to 127 tokens before it, or, where G = h_q / h_kv does not
+ * divide 128 and row tiles of floor(128 / G) tokens reach across the tiles of
+ * 128 keys, up to 126 + floor(128 / G).  So what stands in v behind a batch row's
+ * last token of interest (padding) has to be finite, or the prompts packed by
+ * cu_seqlens, where everything behind a sequence is kept out. */
 HSA_API hsa_status_t hsa_prompt_fwd(const hsa_prompt_shape_t *shape, const void *q, const void *k,
                                     const void *v, const int32_t *cu_seqlens, void *o, float *lse,
                                     void *ws, size_t ws_bytes, void *stream);
